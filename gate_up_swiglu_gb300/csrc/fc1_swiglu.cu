@@ -30,18 +30,14 @@
 // Every wait on an mbarrier gives up after kTimeoutNs of %globaltimer time,
 // raises the sticky flag g_fc1_timeout and lets the pair drain and free its
 // tensor memory, so a fault in the pipeline cannot hang the GPU.
-#include <cuda.h>  // CUtensorMap and its encoding enums (the encoder is fetched at run time)
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-
-#include <atomic>
-#include <cstdint>
-
 #include "abi_internal.h"
 #include "swiglu.h"
 #include "swiglu_kernels.cuh"
+#include "tc_pair.cuh"
 
 namespace fc1 {
+
+using namespace tc;
 
 constexpr int BM = 128;           // rows of X per tile (MMA M)
 constexpr int BN = 128;           // output columns per tile
@@ -52,149 +48,19 @@ constexpr int BK = 64;
 constexpr int SWZ_BYTES = BK * 2;             // bytes per swizzled row
 constexpr int UMMA_K = 16;                    // K per tcgen05.mma of kind::f16
 constexpr int A_BYTES = BM * BK * 2;          // this CTA's 128 rows of X
-static_assert(SWZ_BYTES == 64 || SWZ_BYTES == 128, "64- or 128-byte swizzle");
+static_assert(SWZ_BYTES == 128, "the matrix descriptors are those of the 128-byte swizzle");
 constexpr int TMEM_COLS = 2 * UMMA_N;  // two accumulators
 constexpr int kThreads = 192;
 constexpr int kBarrierBytes = 256;
 constexpr int RING_BYTES = 192 * 1024;
 constexpr int SMEM_BYTES = RING_BYTES + kBarrierBytes + 1024;  // ring + barriers + alignment slack
-constexpr unsigned long long kTimeoutNs = 2000000000ull;                  // 2 s
 
 __device__ int g_fc1_timeout = 0;
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-
-// kCluster: acquire at cluster scope, for data another CTA of the cluster
-// wrote before its release arrive on this barrier.
-template <bool kCluster>
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    if (kCluster)
-        asm volatile(
-            "{\n"
-            ".reg .pred p;\n"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            "selp.u32 %0, 1, 0, p;\n"
-            "}\n"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n"
-            ".reg .pred p;\n"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-            "selp.u32 %0, 1, 0, p;\n"
-            "}\n"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    return ok != 0;
-}
-
-// Wait for the phase of `bar` with the given parity; false (and the timeout
-// flag raised) if it does not complete within kTimeoutNs.
+// tc::mbar_wait_or_flag on this kernel's sticky flag.
 template <bool kCluster = false>
-__device__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait<kCluster>(bar, parity)) return true;
-    const uint64_t t0 = now_ns();
-    while (!mbar_try_wait<kCluster>(bar, parity)) {
-        if (now_ns() - t0 > kTimeoutNs) {
-            atomicExch(&g_fc1_timeout, 1);
-            return false;
-        }
-    }
-    return true;
-}
-
-// Shared-memory matrix descriptor of a K-major operand laid out by TMA with
-// the SWZ_BYTES swizzle: rows of SWZ_BYTES bytes, 8-row groups 8 * SWZ_BYTES
-// apart (stride byte offset), descriptor version 1 (bits 46-47), layout type
-// in bits 61-63 (2 = 128-byte swizzle, 4 = 64-byte swizzle).  The leading
-// byte offset is unused in the swizzled K-major layouts.
-__device__ __forceinline__ uint64_t smem_desc_swizzled(uint32_t saddr) {
-    constexpr uint64_t layout = SWZ_BYTES == 128 ? 2 : 4;
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(16u >> 4) << 16;
-    d |= (uint64_t)((8u * SWZ_BYTES) >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= layout << 61;
-    return d;
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// 32 consecutive fp32 accumulator columns of this warp's 32 TMEM lanes (one
-// lane = one row per thread).
-__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
-          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
-          "=r"(v[31])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_wait_ld() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// outputs are written once and not reread here: evict-first, so they do not
-// push the reused X and W tiles out of L2
-__device__ __forceinline__ void store16(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
-}
-// 32 bytes (sm_100-class 256-bit store): a whole sector
-__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
-    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
-// The 16 words of 32 output columns of one row, from column `col` on (n % 8
-// == 0, so a 16-byte piece is all inside or all outside the row): as two
-// 32-byte stores when `wide` (rows and base 32-byte aligned), else four.
-__device__ __forceinline__ void store_row_chunk(__nv_bfloat16 *p, const uint32_t (&w)[16], int col, int n,
-                                                bool wide) {
-    if (wide) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            if (col + 16 * q < n) store32(p + 16 * q, w + 8 * q);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (col + 8 * q < n) store16(p + 8 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    }
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    return mbar_wait_or_flag<kCluster>(bar, parity, &g_fc1_timeout);
 }
 
 // Two fp32 lanes per instruction: swiglu::x2 and friends (.f32x2 arithmetic,
@@ -295,108 +161,6 @@ static_assert(OFF_ABORT + 4 <= kBarrierBytes, "barriers and state fit their regi
 // 0), N / 8 in bits 17-22, M / 16 in bits 24-28 (M = 256 across the pair).
 constexpr uint32_t kInstrDesc2 = (1u << 4) | (1u << 7) | (1u << 10) |
                                  ((uint32_t)(UMMA_N >> 3) << 17) | ((uint32_t)(PAIR_M >> 4) << 24);
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// The shared::cluster address of this CTA's shared variable `addr` in CTA `rank`.
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
-    uint32_t out;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
-    return out;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// TMA load into this CTA's shared memory whose completion is counted on an
-// mbarrier that may live in the peer CTA (the leader's).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map,
-                                                 uint32_t bar_cluster, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t acc) {
-    asm volatile(
-        "{\n"
-        ".reg .pred p;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(tmem_d),
-        "l"(a), "l"(b), "r"(kInstrDesc2), "r"(acc)
-        : "memory");
-}
-
-// Arrive on the mbarrier at this offset in both CTAs once the pair MMAs issued
-// so far are done.
-__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_commit_local_pair(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-                 : "memory");
-}
-
-// Cluster launch control: ask to cancel the launch of a cluster of this grid
-// that has not started; the 16-byte answer is written at `resp` (this CTA's
-// shared memory) and completes 16 bytes of transaction on `bar`.
-__device__ __forceinline__ void clc_try_cancel(uint32_t resp, uint32_t bar) {
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-            resp),
-        "r"(bar)
-        : "memory");
-}
-
-// The x index of the first CTA of the cluster whose launch was cancelled, or
-// -1 when the request failed (no cluster was left to take).
-__device__ __forceinline__ int clc_cancelled_cta(uint32_t resp) {
-    uint32_t ok, x = 0;
-    asm volatile(
-        "{\n"
-        ".reg .b128 r;\n"
-        ".reg .pred p;\n"
-        "ld.shared.b128 r, [%2];\n"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
-        "selp.u32 %0, 1, 0, p;\n"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n"
-        "}\n"
-        : "=r"(ok), "=r"(x)
-        : "r"(resp)
-        : "memory");
-    return ok ? (int)x : -1;
-}
-
-// Write a tile id (-1: none left) into slot `slot` of both CTAs' tile rings
-// and release it with an arrive on each CTA's tile_full barrier.
-__device__ __forceinline__ void publish_tile(uint32_t ids, uint32_t tile_full0, int slot, int tile) {
-#pragma unroll
-    for (uint32_t r = 0; r < 2; ++r) {
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(ids + 4 * slot, r)), "r"(tile)
-                     : "memory");
-        mbar_arrive_cluster(map_to_rank(tile_full0 + 8 * slot, r));
-    }
-}
 
 __device__ __forceinline__ void pair_tile_coords(int t, int tiles_m2, int tiles_n, int &m0, int &j0) {
     const int per_group = kGroupM * tiles_n;
@@ -573,9 +337,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < BK / UMMA_K; ++kk) {
-                    const uint64_t a = smem_desc_swizzled(sa + s * A_BYTES + kk * UMMA_K * 2);
-                    const uint64_t b = smem_desc_swizzled(sb + s * B2_BYTES + kk * UMMA_K * 2);
-                    mma_bf16_pair(d, a, b, (kb | kk) != 0 ? 1u : 0u);
+                    const uint64_t a = smem_desc_128b(sa + s * A_BYTES + kk * UMMA_K * 2);
+                    const uint64_t b = smem_desc_128b(sb + s * B2_BYTES + kk * UMMA_K * 2);
+                    mma_bf16_pair(d, a, b, kInstrDesc2, (kb | kk) != 0 ? 1u : 0u);
                 }
                 mma_commit_both(empty0 + 8 * s);
             }
@@ -669,30 +433,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- host side
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-std::atomic<EncodeTiled> g_encode{nullptr};
-
 swiglu_status_t fail(cudaError_t e) {
     swiglu_abi::record_cuda_error((int)e);
     return SWIGLU_ERR_CUDA;
-}
-
-cudaError_t encoder(EncodeTiled &fn) {
-    fn = g_encode.load();
-    if (fn != nullptr) return cudaSuccess;
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                                     cudaEnableDefault, &q);
-    if (e != cudaSuccess) return e;
-    if (q != cudaDriverEntryPointSuccess || p == nullptr) return cudaErrorNotSupported;
-    fn = reinterpret_cast<EncodeTiled>(p);
-    g_encode.store(fn);
-    return cudaSuccess;
 }
 
 // [rows, K] bf16, row-major: a box of BK K-elements (SWZ_BYTES bytes) by 128
@@ -703,8 +446,7 @@ bool make_map(EncodeTiled enc, CUtensorMap *map, const void *base, int64_t rows,
     const cuuint32_t box[2] = {(cuuint32_t)BK, 128};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               SWZ_BYTES == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -1,0 +1,290 @@
+// tc_pair.cuh -- building blocks of the tensor-core kernels (tcgen05, TMEM,
+// TMA, clusters of two CTAs, cluster launch control), shared by linear_fc1 and
+// the routed experts' products.
+#pragma once
+
+#include <cuda.h>  // CUtensorMap and its encoding enums (the encoder is fetched at run time)
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+namespace tc {
+
+constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
+// kCluster: acquire at cluster scope, for data another CTA of the cluster
+// wrote before its release arrive on this barrier.
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    if (kCluster)
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n"
+            "}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n"
+            "}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    return ok != 0;
+}
+
+// Wait for the phase of `bar` with the given parity; false (and *flag raised)
+// if it does not complete within kTimeoutNs.
+template <bool kCluster = false>
+__device__ bool mbar_wait_or_flag(uint32_t bar, uint32_t parity, int *flag) {
+    if (mbar_try_wait<kCluster>(bar, parity)) return true;
+    const uint64_t t0 = now_ns();
+    while (!mbar_try_wait<kCluster>(bar, parity)) {
+        if (now_ns() - t0 > kTimeoutNs) {
+            atomicExch(flag, 1);
+            return false;
+        }
+    }
+    return true;
+}
+
+// Shared-memory matrix descriptor of a bf16 operand laid out by TMA with the
+// 128-byte swizzle: the start address, the leading and stride byte offsets, the
+// descriptor version 1 (bits 46-47) and the layout type 2 (bits 61-63).
+//   K-major (rows of 64 K elements): 8-row groups `sbo` = 1024 bytes apart; the
+//     leading offset is unused.
+//   MN-major (rows of 64 M or N elements, one row per K): groups of 8 K `sbo` =
+//     1024 bytes apart, groups of 64 M or N `lbo` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_128b(uint32_t saddr, uint32_t lbo = 16, uint32_t sbo = 1024) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(sbo >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// 32 consecutive fp32 accumulator columns of this warp's 32 TMEM lanes (one
+// lane = one row per thread).
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+          "=r"(v[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait_ld() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// outputs are written once and not reread here: evict-first, so they do not
+// push the reused X and W tiles out of L2
+__device__ __forceinline__ void store16(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+// 32 bytes (sm_100-class 256-bit store): a whole sector
+__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
+    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// The 16 words of 32 output columns of one row, from column `col` on (n % 8
+// == 0, so a 16-byte piece is all inside or all outside the row): as two
+// 32-byte stores when `wide` (rows and base 32-byte aligned), else four.
+__device__ __forceinline__ void store_row_chunk(__nv_bfloat16 *p, const uint32_t (&w)[16], int col, int n,
+                                                bool wide) {
+    if (wide) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (col + 16 * q < n) store32(p + 16 * q, w + 8 * q);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (col + 8 * q < n) store16(p + 8 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The shared::cluster address of this CTA's shared variable `addr` in CTA `rank`.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+    uint32_t out;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
+    return out;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// TMA load into this CTA's shared memory whose completion is counted on an
+// mbarrier that may live in the peer CTA (the leader's).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map,
+                                                 uint32_t bar_cluster, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t acc) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// The same for a tensor map of three dimensions.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map,
+                                                 uint32_t bar_cluster, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// Arrive on the mbarrier at this offset in both CTAs once the pair MMAs issued
+// so far are done.
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_local_pair(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+                 : "memory");
+}
+
+// Cluster launch control: ask to cancel the launch of a cluster of this grid
+// that has not started; the 16-byte answer is written at `resp` (this CTA's
+// shared memory) and completes 16 bytes of transaction on `bar`.
+__device__ __forceinline__ void clc_try_cancel(uint32_t resp, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            resp),
+        "r"(bar)
+        : "memory");
+}
+
+// The x index of the first CTA of the cluster whose launch was cancelled, or
+// -1 when the request failed (no cluster was left to take).
+__device__ __forceinline__ int clc_cancelled_cta(uint32_t resp) {
+    uint32_t ok, x = 0;
+    asm volatile(
+        "{\n"
+        ".reg .b128 r;\n"
+        ".reg .pred p;\n"
+        "ld.shared.b128 r, [%2];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n"
+        "}\n"
+        : "=r"(ok), "=r"(x)
+        : "r"(resp)
+        : "memory");
+    return ok ? (int)x : -1;
+}
+
+// Write a tile id (-1: none left) into slot `slot` of both CTAs' tile rings
+// and release it with an arrive on each CTA's tile_full barrier.
+__device__ __forceinline__ void publish_tile(uint32_t ids, uint32_t tile_full0, int slot, int tile) {
+#pragma unroll
+    for (uint32_t r = 0; r < 2; ++r) {
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(ids + 4 * slot, r)), "r"(tile)
+                     : "memory");
+        mbar_arrive_cluster(map_to_rank(tile_full0 + 8 * slot, r));
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline std::atomic<EncodeTiled> g_encode{nullptr};
+
+// cuTensorMapEncodeTiled, looked up once.
+inline cudaError_t encoder(EncodeTiled &fn) {
+    fn = g_encode.load();
+    if (fn != nullptr) return cudaSuccess;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                     cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || p == nullptr) return cudaErrorNotSupported;
+    fn = reinterpret_cast<EncodeTiled>(p);
+    g_encode.store(fn);
+    return cudaSuccess;
+}
+
+}  // namespace tc
