@@ -514,3 +514,9 @@ __all__ = ["swiglu_gateup_fwd", "swiglu_gateup_bwd", "swiglu_silu_mul_fwd", "swi
            "swiglu_fc1_fwd", "fc1_timeout_flag", "host_staging_bytes",
            "swiglu_gateup_fwd_bwd_host", "status_string", "SwigluError", "lib",
            "SWIGLU_F32", "SWIGLU_BF16", "EXPORTS", "LIB_PATH"]
+
+# the routed experts' operators (they use the helpers above)
+from .moe import *  # noqa: E402,F401,F403
+from .moe import __all__ as _moe_all  # noqa: E402
+
+__all__ += _moe_all

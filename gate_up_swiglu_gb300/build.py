@@ -5,10 +5,10 @@
 Run it as a script (or load it by path): importing the package itself needs
 the built library.
 
-The library is three translation units (the C ABI with the streaming kernel
-templates it instantiates, the tensor-core linear_fc1 + SwiGLU kernel, and the
-host-buffer pipeline),
-compiled in parallel and linked against the static CUDA runtime so the .so depends on
+The library is five translation units (the C ABI with the streaming kernel
+templates it instantiates, the tensor-core linear_fc1 + SwiGLU kernel, the
+host-buffer pipeline, the 8-bit activation checkpoint and the routed experts'
+products), compiled in parallel and linked against the static CUDA runtime so the .so depends on
 nothing but the NVIDIA driver (libcuda).  No fast-math: the kernels choose every approximate
 operation explicitly and must keep subnormal results.
 """
@@ -25,7 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libswiglu.so")
 SOURCES = [os.path.join(CSRC, "swiglu_abi.cu"), os.path.join(CSRC, "fc1_swiglu.cu"),
-           os.path.join(CSRC, "host_pipeline.cu")]
+           os.path.join(CSRC, "host_pipeline.cu"), os.path.join(CSRC, "ckpt8.cu"),
+           os.path.join(CSRC, "grouped_mm.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

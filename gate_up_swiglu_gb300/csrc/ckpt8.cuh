@@ -1,0 +1,320 @@
+// ckpt8.cuh -- device code of the 8-bit activation checkpoint: e4m3 codes with
+// one power-of-two scale per block of 32 columns (the format of swiglu_moe.h).
+#pragma once
+
+#include <stdint.h>
+
+#include "swiglu_kernels.cuh"
+
+namespace ckpt8 {
+
+constexpr int kBlock = 32;
+
+// Largest finite |v| of a thread's values.  fmaxf drops NaN; infinities are
+// rare enough to be looked for only once one has turned up.
+template <int N>
+__device__ __forceinline__ float finite_amax(const float *v) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
+    if (m == INFINITY) {
+        m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]) == INFINITY ? 0.0f : fabsf(v[i]));
+    }
+    return m;
+}
+
+// The smallest code c >= 0 with amax <= 448 * 2^(c - 127), 448 = 1.75 * 2^8:
+// with amax = m 2^k (1 <= m < 2), c = k - 8 + 127, one more when m > 1.75.
+// Adding 0x1fffff to the bits carries into the exponent exactly for mantissas
+// above .75.
+__device__ __forceinline__ uint32_t scale_code(float amax) {
+    const int c = (int)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 8;
+    return (uint32_t)max(c, 0);
+}
+
+// 2^(127 - c) and 2^(c - 127), exact (c <= 247; 2^-127 is a subnormal).
+__device__ __forceinline__ float encode_factor(uint32_t c) { return __uint_as_float((254u - c) << 23); }
+__device__ __forceinline__ float decode_factor(uint32_t c) {
+    return __uint_as_float(c == 0 ? 1u << 22 : c << 23);
+}
+
+// Two values to e4m3, nearest even; `lo` in the low byte.  The conversion
+// saturates, so an infinity is made a NaN first (finite values of a block are
+// at most 448 after scaling).
+__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
+    unsigned short h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+
+// N values (N = 1 or a multiple of 2) scaled by `f` to N codes.  The largest
+// values of fp32 would round up to 256 * 2^120 = 2^128, which fp32 cannot hold:
+// they keep the code of 240.  One test of the largest value tells whether any
+// of this, or an infinity, has to be looked at.
+template <int N>
+__device__ __forceinline__ void encode(const float *v, float f, uint32_t *out) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
+    const bool rare = m > 2.97747071e38f;  // 1.75 * 2^127
+    const float top = f == 7.52316384526264e-37f ? 240.0f : 448.0f;  // 2^-120: the largest scale
+    const auto one = [&](int i) {
+        float t = __fmul_rn(v[i], f);
+        if (rare) t = fabsf(v[i]) == INFINITY ? __uint_as_float(0x7fc00000u) : t > top ? top : t < -top ? -top : t;
+        return t;
+    };
+    if (N == 1) {
+        out[0] = codes2(one(0), 0.0f) & 0xffu;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const uint32_t h = codes2(one(i), one(i + 1));
+            if (i % 4 == 0)
+                out[i / 4] = h;
+            else
+                out[i / 4] |= h << 16;
+        }
+    }
+}
+
+// N codes to the values they stand for (e4m3 is exact in fp16 and fp32).
+template <int N>
+__device__ __forceinline__ void decode(const uint32_t *q, float f, float *v) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const unsigned short h = (unsigned short)(q[i / 4] >> (i % 4 * 8));
+        uint32_t pair;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(pair) : "h"(h));
+        float lo, hi;
+        asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.f32.f16 %0, a;\ncvt.f32.f16 %1, b;\n}\n"
+            : "=f"(lo), "=f"(hi)
+            : "r"(pair));
+        v[i] = __fmul_rn(lo, f);
+        if (i + 1 < N) v[i + 1] = __fmul_rn(hi, f);
+    }
+}
+
+// N code bytes of a pack (N = 1, 4, 8 or 16), as words.
+template <int N, int LD>
+__device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t *w) {
+    if constexpr (N == 1)
+        w[0] = *p;
+    else
+        swiglu::Ld<N, LD>::run(p, w);
+}
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t *w) {
+    if constexpr (N == 1)
+        *p = (uint8_t)w[0];
+    else
+        swiglu::St<N, swiglu::kStStream>::run(p, w);
+}
+
+// ---------------------------------------------------------------- kernels ---
+// Both are one pass over the data: the forward reads x (2 elements a pair) and
+// writes y, two codes and 2/32 scale bytes; the backward reads dy, the codes
+// and scales and writes dx (and y).  In bf16 that is 8.06 bytes a pair either
+// way for about 15 (forward) and 20 (backward) instructions, so both are bound
+// by HBM.
+//
+// A pack is VEC elements of one half; a block of 32 columns is 32 / VEC
+// neighbouring lanes, so the forward's block maximum is a shuffle inside that
+// lane group.  Rows are padded to whole blocks in the pack index (rows *
+// blocks * 32 / VEC packs in all), which keeps a block's lanes together in one
+// warp whatever n is.
+
+struct FwdParams {
+    const char *x;
+    const float *w;  // [rows], or null
+    char *y;
+    uint8_t *q;
+    uint8_t *scales;
+    int64_t rows, n;
+    int64_t x_stride, y_stride;  // bytes
+    int64_t q_stride, s_stride;
+    int64_t packs;               // rows * packs per row
+    swiglu::FastDiv div;         // by the packs per row
+    int32_t row_packs;
+    int32_t blocks;              // per half
+};
+
+template <typename E, int VEC, int T>
+__global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
+    swiglu::await_previous_grid();
+    swiglu::allow_next_grid();
+    constexpr int B = E::kBytes * VEC;
+    constexpr int NW = (B + 3) / 4;
+    constexpr int kLanes = kBlock / VEC;  // lanes of a block
+    constexpr int QW = (VEC + 3) / 4;
+    // the loop's condition is the same for a whole warp: the shuffles need it
+    for (int64_t v0 = (int64_t)blockIdx.x * T + (threadIdx.x & ~31); v0 < p.packs; v0 += (int64_t)gridDim.x * T) {
+        const int64_t v = v0 + (threadIdx.x & 31);
+        const int64_t r = swiglu::fast_div(v, p.div);
+        const int32_t c = (int32_t)(v - r * p.row_packs);
+        const int64_t col = (int64_t)c * VEC;
+        const bool live = v < p.packs && col < p.n;
+        uint32_t gw[NW] = {}, uw[NW] = {};
+        float wr = 1.0f;
+        if (live) {
+            const char *xr = p.x + r * p.x_stride + col * E::kBytes;
+            swiglu::Ld<B, swiglu::kLdNC>::run(xr, gw);
+            swiglu::Ld<B, swiglu::kLdNC>::run(xr + p.n * E::kBytes, uw);
+            if (p.w != nullptr) wr = __ldg(p.w + r);
+        }
+        float g[VEC], u[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            g[i] = E::get(gw, i);
+            u[i] = E::get(uw, i);
+        }
+        float mg = finite_amax<VEC>(g), mu = finite_amax<VEC>(u);
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) {
+            mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+            mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+        }
+        if (!live) continue;
+        const uint32_t cg = scale_code(mg), cu = scale_code(mu);
+        uint32_t qg[QW], qu[QW];
+        encode<VEC>(g, encode_factor(cg), qg);
+        encode<VEC>(u, encode_factor(cu), qu);
+        uint8_t *qr = p.q + r * p.q_stride + col;
+        store_codes<VEC>(qr, qg);
+        store_codes<VEC>(qr + p.n, qu);
+        if (c % kLanes == 0) {
+            uint8_t *sr = p.scales + r * p.s_stride + c / kLanes;
+            sr[0] = (uint8_t)cg;
+            sr[p.blocks] = (uint8_t)cu;
+        }
+        float yv[VEC];
+        if (swiglu::pack_has_deep<E, VEC>(gw))
+            swiglu::fwd_pack<E, VEC, swiglu::kWeight, true>(gw, uw, nullptr, nullptr, wr, yv);
+        else
+            swiglu::fwd_pack<E, VEC, swiglu::kWeight, false>(gw, uw, nullptr, nullptr, wr, yv);
+        uint32_t o[NW] = {};
+        swiglu::store_pack<E, VEC>(o, yv);
+        swiglu::St<B, swiglu::kStStream>::run(p.y + r * p.y_stride + col * E::kBytes, o);
+    }
+}
+
+struct BwdParams {
+    const char *dy;
+    const uint8_t *q;
+    const uint8_t *scales;
+    const float *w;  // [rows], or null
+    char *dx;
+    float *dw;       // [rows], or null
+    char *y;         // or null
+    int64_t rows, n;
+    int64_t dy_stride, dx_stride, y_stride;  // bytes
+    int64_t q_stride, s_stride;
+    int64_t packs;
+    swiglu::FastDiv div;
+    int32_t row_packs;  // ceil(n / VEC)
+    int32_t blocks;
+};
+
+// One pack: dg, du, y (all with the row weight) and the dw terms added up.
+template <typename E, int VEC, int MODE, bool kMayDeep>
+__device__ __forceinline__ void bwd_values(const uint32_t *d, const float *g, const float *u, float wr, float &acc,
+                                           float *dg, float *du, float *yv) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const float df = E::get(d, i);
+        const swiglu::Act act = swiglu::activation<E, true, kMayDeep>(g[i]);
+        float y = __fmul_rn(act.silu, u[i]);
+        float dd = df;
+        if (MODE & swiglu::kWeight) {
+            float term = __fmul_rn(df, y);
+            if (kMayDeep) term = __fmul_rn(term, act.scale);
+            acc = __fadd_rn(acc, term);
+            dd = __fmul_rn(df, wr);
+            y = __fmul_rn(y, wr);
+        }
+        dg[i] = __fmul_rn(dd, __fmul_rn(u[i], act.dsilu));
+        du[i] = __fmul_rn(dd, act.silu);
+        if (kMayDeep) {
+            dg[i] = __fmul_rn(dg[i], act.scale);
+            du[i] = __fmul_rn(du[i], act.scale);
+            y = __fmul_rn(y, act.scale);
+        }
+        yv[i] = y;
+    }
+}
+
+template <typename E, int VEC, int MODE>
+__device__ __forceinline__ void bwd_one(const BwdParams &p, int64_t r, int32_t c, float wr, float &acc) {
+    constexpr int B = E::kBytes * VEC;
+    constexpr int NW = (B + 3) / 4;
+    constexpr int QW = (VEC + 3) / 4;
+    const int64_t col = (int64_t)c * VEC;
+    uint32_t d[NW], qg[QW], qu[QW];
+    const uint8_t *qr = p.q + r * p.q_stride + col;
+    const uint8_t *sr = p.scales + r * p.s_stride + col / kBlock;
+    swiglu::Ld<B, swiglu::kLdNC>::run(p.dy + r * p.dy_stride + col * E::kBytes, d);
+    load_codes<VEC, swiglu::kLdNC>(qr, qg);
+    load_codes<VEC, swiglu::kLdNC>(qr + p.n, qu);
+    const uint32_t cg = __ldg(sr), cu = __ldg(sr + p.blocks);
+    float g[VEC], u[VEC], dg[VEC], du[VEC], yv[VEC];
+    decode<VEC>(qg, decode_factor(cg), g);
+    decode<VEC>(qu, decode_factor(cu), u);
+    float gmin = g[0];
+#pragma unroll
+    for (int i = 1; i < VEC; ++i) gmin = fminf(gmin, g[i]);
+    if (E::kDeepScale && gmin < -64.0f)
+        bwd_values<E, VEC, MODE, true>(d, g, u, wr, acc, dg, du, yv);
+    else
+        bwd_values<E, VEC, MODE, false>(d, g, u, wr, acc, dg, du, yv);
+    uint32_t og[NW] = {}, ou[NW] = {};
+    swiglu::store_pack<E, VEC>(og, dg);
+    swiglu::store_pack<E, VEC>(ou, du);
+    char *dxr = p.dx + r * p.dx_stride + col * E::kBytes;
+    swiglu::St<B, swiglu::kStStream>::run(dxr, og);
+    swiglu::St<B, swiglu::kStStream>::run(dxr + p.n * E::kBytes, ou);
+    if (p.y != nullptr) {
+        uint32_t oy[NW] = {};
+        swiglu::store_pack<E, VEC>(oy, yv);
+        swiglu::St<B, swiglu::kStStream>::run(p.y + r * p.y_stride + col * E::kBytes, oy);
+    }
+}
+
+// Without weights: the flattened pack index, one pack per thread.
+template <typename E, int VEC, int T>
+__global__ void __launch_bounds__(T) ckpt8_bwd_kernel(const BwdParams p) {
+    swiglu::await_previous_grid();
+    swiglu::allow_next_grid();
+    float acc = 0.0f;
+    for (int64_t v = (int64_t)blockIdx.x * T + threadIdx.x; v < p.packs; v += (int64_t)gridDim.x * T) {
+        const int64_t r = swiglu::fast_div(v, p.div);
+        bwd_one<E, VEC, swiglu::kPlain>(p, r, (int32_t)(v - r * p.row_packs), 1.0f, acc);
+    }
+}
+
+// With weights: a CTA takes a row, so dw[r] is a sum inside the CTA in a fixed
+// order.
+template <typename E, int VEC, int T>
+__global__ void __launch_bounds__(T) ckpt8_bwd_weighted_kernel(const BwdParams p) {
+    swiglu::await_previous_grid();
+    swiglu::allow_next_grid();
+    __shared__ float red[T / 32];
+    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        const float wr = __ldg(p.w + r);
+        float acc = 0.0f;
+        for (int32_t c = threadIdx.x; c < p.row_packs; c += T) bwd_one<E, VEC, swiglu::kWeight>(p, r, c, wr, acc);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
+        __syncthreads();  // red may still be read for the previous row
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float t = 0.0f;
+#pragma unroll
+            for (int k = 0; k < T / 32; ++k) t = __fadd_rn(t, red[k]);
+            p.dw[r] = t;
+        }
+    }
+}
+
+}  // namespace ckpt8

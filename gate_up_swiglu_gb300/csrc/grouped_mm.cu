@@ -1,0 +1,1005 @@
+// grouped_mm.cu -- the routed experts' matrix products on the tensor cores
+// (tcgen05, TMEM, TMA, CTA pairs): one weight matrix per expert, rows sorted by
+// expert, ragged groups.
+//
+//   forward      y[t]  = W[e] x[t]                 (kMm)
+//   first layer  y[t]  = probs[t] silu(Wg[e] x[t]) * (Wu[e] x[t])   (kFc1)
+//   data grad    dx[t] = W[e]^T dy[t]              (kDgrad)
+//   weight grad  dW[e] = sum_t dy[t]^T x[t]        (kWgrad)
+//
+// A cluster of two CTAs computes a tile with tcgen05.mma.cta_group::2 (M = 256:
+// 128 accumulator lanes in each CTA's tensor memory; N a multiple of 32 up to
+// 256; bf16 in, fp32 accumulate).  In the three products over rows the FEATURES
+// (rows of W, or its columns for the data gradient) are the M side and the rows
+// t are the N side: N is a field of the instruction, so the last tile of a
+// group is as wide as its rows need, to 32, where rows on the M side would pad
+// every group to 256 (with 64 groups of 128 rows on average, half the work).
+// The weight gradient has W's rows as M and its columns as N.
+//
+// Operand tiles are 64 elements of the contraction deep, 128-byte swizzle.
+// Where the contraction runs along memory rows the tile is K-major; the data
+// gradient's W and both operands of the weight gradient have it across memory
+// rows and are loaded as they lie (MN-major descriptors): nothing is
+// transposed in memory.
+//
+// The roles of the 192 threads (224 for the weight gradient) of a CTA, the ring
+// of six 32 KiB stages, the two accumulators and the scheduling by cluster
+// launch control are those of fc1_swiglu.cu.  The number of tiles depends on
+// the groups, which only the device knows: the grid holds as many clusters as
+// the sizes allow at most, and a pair that finds its tile beyond the last one
+// drops it.
+//
+// The weight gradient's contraction runs over a group's rows, so its last block
+// of 64 would take in rows of the next group.  Those loads are counted on a
+// barrier of their own, warp 6 of each CTA zeroes the rows beyond the group in
+// shared memory (a product with 0 would not do: a neighbour's row may hold
+// NaN), and only then the stage is handed to the tensor cores.
+#include <climits>
+
+#include "ckpt8.cuh"
+#include "moe_host.h"
+#include "swiglu_kernels.cuh"
+#include "tc_pair.cuh"
+
+namespace gmm {
+
+using namespace tc;
+
+enum : int { kFc1 = 0, kMm = 1, kDgrad = 2, kWgrad = 3 };
+
+constexpr int BK = 64;               // contraction elements per stage
+constexpr int UMMA_K = 16;           // per tcgen05.mma of kind::f16
+constexpr int TILE_N = 256;          // accumulator columns per tile at most
+constexpr int A_BYTES = 128 * BK * 2;            // a CTA's half of the M side
+constexpr int STAGE_BYTES = 2 * A_BYTES;         // and at most as much of the N side
+constexpr int STAGES = 6;
+constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+constexpr int TMEM_COLS = 2 * TILE_N;            // two accumulators
+constexpr int kMaxGroups = SWIGLU_MAX_GROUPS;
+constexpr int kGroupN = 16;          // N tiles per block of the tile order
+// fp32 weight gradients are summed in segments of this many rows: the tensor
+// cores' fp32 accumulation drops low bits at every step (a relative error of
+// about 1.1e-9 per row summed was measured: 4.4e-6 over 4096), and the segments
+// are added with rounded fp32 additions
+constexpr int kSegmentRows = 4096;
+
+constexpr int kTileSlots = 4;
+constexpr int kAskAhead = 16;
+// byte offsets in the region after the ring
+constexpr int OFF_FULL = 0;
+constexpr int OFF_EMPTY = OFF_FULL + 8 * STAGES;
+constexpr int OFF_TAIL = OFF_EMPTY + 8 * STAGES;          // this CTA's loads of a group's last rows (kWgrad)
+constexpr int OFF_ACC_FULL = OFF_TAIL + 8 * STAGES;
+constexpr int OFF_ACC_EMPTY = OFF_ACC_FULL + 16;
+constexpr int OFF_MMA_DONE = OFF_ACC_EMPTY + 16;
+constexpr int OFF_TILE_FULL = OFF_MMA_DONE + 8;
+constexpr int OFF_TILE_EMPTY = OFF_TILE_FULL + 8 * kTileSlots;
+constexpr int OFF_CLC_BAR = OFF_TILE_EMPTY + 8 * kTileSlots;
+constexpr int OFF_CLC_RESP = (OFF_CLC_BAR + 8 + 15) / 16 * 16;
+constexpr int OFF_TILE_ID = OFF_CLC_RESP + 16;
+constexpr int OFF_TMEM = OFF_TILE_ID + 4 * kTileSlots;
+constexpr int OFF_ABORT = OFF_TMEM + 4;
+constexpr int STATE_BYTES = 512;
+static_assert(OFF_ABORT + 4 <= STATE_BYTES, "barriers and state fit their region");
+// the epilogue's staging: 32 rows of 32 features per warp, or of 32 gates and
+// 32 ups per pair of warps (kFc1), fp32, rows padded by 4 words
+constexpr int STG_ROW = 36, STG_ROW_FC1 = 68;
+constexpr int STG_WARP_BYTES = 32 * STG_ROW * 4;
+constexpr int STG_BYTES = 4 * STG_WARP_BYTES;
+static_assert(32 * STG_ROW_FC1 * 4 <= 2 * STG_WARP_BYTES, "a pair of warps has the room of two");
+constexpr int TABLE_BYTES = 2 * (kMaxGroups + 2) * 4;
+constexpr int SMEM_BYTES = RING_BYTES + STATE_BYTES + STG_BYTES + (TABLE_BYTES + 15) / 16 * 16 + 1024;
+static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM");
+
+__device__ int g_timeout = 0;
+
+template <bool kCluster = false>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    return mbar_wait_or_flag<kCluster>(bar, parity, &g_timeout);
+}
+
+// Arrive on a barrier of the cluster, expecting `bytes` more.
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar_cluster, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster),
+                 "r"(bytes)
+                 : "memory");
+}
+
+struct Params {
+    CUtensorMap a;     // the M side
+    CUtensorMap b[4];  // the N side, boxes of 16, 32, 64 and 128 rows (kWgrad: b[0] alone, 64 rows)
+    const int32_t *ends;
+    const float *probs;      // kFc1
+    void *out;               // y, dx or dW
+    __nv_bfloat16 *fc1;      // kFc1: what the backward keeps
+    uint8_t *q;
+    uint8_t *scales;
+    int rows, groups;
+    int features;    // kFc1: n; kMm: N; kDgrad: K; kWgrad: N
+    int cols;        // kWgrad: K
+    int depth;       // contraction length (kWgrad: unused)
+    int f32_out, accumulate;  // kWgrad
+};
+
+// Features of a tile: kFc1 has a gate and an up row for each.
+template <int MODE>
+constexpr int kTileF = MODE == kFc1 ? 128 : 256;
+
+// Where the tiles of a call lie.  starts[e] is group e's first row (e < groups;
+// starts[groups] the first row of no group, starts[groups + 1] = rows) and
+// base[e] its first tile.
+struct Groups {
+    const int *starts;
+    const int *base;
+};
+
+struct Tile {
+    int group, m0, n0, cnt;  // first feature, first row (kWgrad: column), rows (kWgrad: columns)
+    int r0, rows;            // the group's rows
+};
+
+// Fill starts and base (one warp).  The last "group" is that of the rows that
+// belong to none.
+template <int MODE>
+__device__ void build_groups(const Params &p, int *starts, int *base) {
+    const int lane = threadIdx.x & 31;
+    const int tf = (p.features + kTileF<MODE> - 1) / kTileF<MODE>;
+    const int per_group = MODE == kWgrad ? tf * ((p.cols + TILE_N - 1) / TILE_N) : 0;
+    int end_before = 0, tiles_before = 0;
+    for (int e0 = 0; e0 <= p.groups; e0 += 32) {
+        const int e = e0 + lane;
+        int end = 0;
+        if (e < p.groups)
+            asm volatile("ld.global.b32 %0, [%1];" : "=r"(end) : "l"(p.ends + e) : "memory");
+        else if (e == p.groups)
+            end = p.rows;
+        end = min(max(end, 0), p.rows);
+        if (lane == 0) end = max(end, end_before);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end = max(end, v);
+        }
+        int start = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) start = end_before;
+        int tiles = 0;
+        if (MODE == kWgrad)
+            tiles = e < p.groups ? per_group : 0;
+        else if (e <= p.groups)
+            tiles = (end - start + TILE_N - 1) / TILE_N * tf;
+        int sum = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (e <= p.groups) {
+            starts[e] = start;
+            base[e] = tiles_before + sum - tiles;
+            starts[e + 1] = end;  // the next lane or round writes the same
+            base[e + 1] = tiles_before + sum;
+        }
+        end_before = __shfl_sync(0xffffffffu, end, 31);
+        tiles_before += __shfl_sync(0xffffffffu, sum, 31);
+        __syncwarp();
+    }
+}
+
+// Tile order: within a group, blocks of up to kGroupN N tiles; within a block
+// the N tile varies fastest, so a slab of W is read from HBM once per block and
+// the block's rows stay in L2.
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(const Params &p, const Groups &g, int t) {
+    int lo = 0, hi = p.groups;  // the last e with base[e] <= t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (g.base[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    Tile o;
+    o.group = lo;
+    o.r0 = g.starts[lo];
+    o.rows = g.starts[lo + 1] - o.r0;
+    const int extent = MODE == kWgrad ? p.cols : o.rows;
+    const int nt = (extent + TILE_N - 1) / TILE_N;
+    const int tf = (p.features + kTileF<MODE> - 1) / kTileF<MODE>;
+    const int local = t - g.base[lo];
+    const int block = local / (kGroupN * tf);
+    const int first = block * kGroupN;
+    const int width = min(kGroupN, nt - first);
+    const int in = local - block * (kGroupN * tf);
+    o.m0 = in / width * kTileF<MODE>;
+    const int j = first + in % width;
+    // equal N tiles, to 32 (the last one may be shorter)
+    const int step = MODE == kWgrad ? TILE_N : ((extent + nt - 1) / nt + 31) / 32 * 32;
+    o.n0 = j * step;
+    o.cnt = min(step, extent - o.n0);
+    return o;
+}
+
+__device__ __forceinline__ float4 lds128(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+
+// 16 bf16 at p, of which the first `live` (a multiple of 8) are stored.
+__device__ __forceinline__ void store_bf16x16(__nv_bfloat16 *p, const uint32_t (&w)[8], int live, bool wide) {
+    if (wide) {
+        if (live > 0) store32(p, w);
+    } else {
+        if (live > 0) store16(p, w[0], w[1], w[2], w[3]);
+        if (live > 8) store16(p + 8, w[4], w[5], w[6], w[7]);
+    }
+}
+
+__device__ __forceinline__ void store_codes16(uint8_t *p, const uint32_t (&w)[4], int live, bool wide) {
+    if (wide) {
+        if (live > 0) store16(p, w[0], w[1], w[2], w[3]);
+    } else {
+        if (live > 0) swiglu::St<8, swiglu::kStStream>::run(p, w);
+        if (live > 8) swiglu::St<8, swiglu::kStStream>::run(p + 8, w + 2);
+    }
+}
+
+// y for 16 gates and ups of one row, from fp32, rounded once: the operations of
+// the streaming kernels (swiglu::activation), with the row weight last.
+template <bool kMayDeep>
+__device__ __forceinline__ void activate16(const float (&g)[16], const float (&u)[16], float w, uint32_t (&out)[8]) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        float r[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const swiglu::Act act = swiglu::activation<swiglu::BF16, false, kMayDeep>(g[i + h]);
+            r[h] = __fmul_rn(__fmul_rn(act.silu, u[i + h]), w);
+            if (kMayDeep) r[h] = __fmul_rn(r[h], act.scale);
+        }
+        swiglu::BF16::put2(out, i, r[0], r[1]);
+    }
+}
+
+// True in both warps of a pair (barrier `id`) when `v` holds in either.
+__device__ __forceinline__ bool any_of_pair(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "setp.ne.u32 p, %2, 0;\n"
+        "bar.red.or.pred q, %1, 64, p;\n"
+        "selp.u32 %0, 1, 0, q;\n"
+        "}\n"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator (bits 4-5 =
+// 1), A and B bf16 (bits 7-9 and 10-12 = 1), A / B MN-major (bits 15, 16), N / 8
+// in bits 17-22, M / 16 in bits 24-28 (M = 256 across the pair).
+__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224 : 192, 1)
+    grouped_mm_kernel(const __grid_constant__ Params p) {
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    unsigned char *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t ring = smem_addr(smem);
+    unsigned char *state = smem + RING_BYTES;
+    const uint32_t st0 = smem_addr(state);
+    const uint32_t full0 = st0 + OFF_FULL, empty0 = st0 + OFF_EMPTY, tail0 = st0 + OFF_TAIL;
+    const uint32_t acc_full0 = st0 + OFF_ACC_FULL, acc_empty0 = st0 + OFF_ACC_EMPTY;
+    const uint32_t mma_done = st0 + OFF_MMA_DONE;
+    const uint32_t tile_full0 = st0 + OFF_TILE_FULL, tile_empty0 = st0 + OFF_TILE_EMPTY;
+    const uint32_t clc_bar = st0 + OFF_CLC_BAR, clc_resp = st0 + OFF_CLC_RESP;
+    const uint32_t tile_ids_addr = st0 + OFF_TILE_ID;
+    volatile int *tile_ids = reinterpret_cast<volatile int *>(state + OFF_TILE_ID);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(state + OFF_ABORT);
+    float *staging = reinterpret_cast<float *>(state + STATE_BYTES);
+    int *starts = reinterpret_cast<int *>(state + STATE_BYTES + STG_BYTES);
+    int *base = starts + kMaxGroups + 2;
+
+    constexpr bool kAMn = MODE == kDgrad || MODE == kWgrad;
+    constexpr bool kBMn = MODE == kWgrad;
+    // readers of a tile id: the peer's producer, the MMA thread, the epilogue
+    // warps of both CTAs and, for the weight gradient, the warps that zero rows
+    constexpr int kReaders = 1 + 1 + 2 * 4 + (MODE == kWgrad ? 2 : 0);
+
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tile_empty_leader0 = map_to_rank(tile_empty0, 0);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            // kWgrad: each CTA arrives for its own half (the producer, or warp 6
+            // once the rows beyond the group are zero)
+            mbar_init(full0 + 8 * s, MODE == kWgrad ? 2 : 1);
+            mbar_init(empty0 + 8 * s, 1);
+            mbar_init(tail0 + 8 * s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(acc_full0 + 8 * a, 1);
+            mbar_init(acc_empty0 + 8 * a, 8);
+        }
+        mbar_init(mma_done, 1);
+        for (int i = 0; i < kTileSlots; ++i) {
+            mbar_init(tile_full0 + 8 * i, 1);
+            mbar_init(tile_empty0 + 8 * i, kReaders);
+        }
+        mbar_init(clc_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    // from here on global memory is read: the previous grid must have completed
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 2) build_groups<MODE>(p, starts, base);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Groups groups = {starts, base};
+    const int tiles = base[p.groups + 1];
+
+    // contraction blocks of a tile
+    const auto blocks_of = [&](const Tile &t) {
+        if (MODE == kWgrad) return (t.rows + BK - 1) / BK;
+        return t.group == p.groups ? 0 : (p.depth + BK - 1) / BK;
+    };
+    // columns of the instruction
+    const auto width_of = [&](const Tile &t) { return MODE == kWgrad ? TILE_N : (t.cnt + 31) / 32 * 32; };
+    // contraction blocks per accumulation (kWgrad with fp32 results: a segment)
+    const int seg_blocks = MODE == kWgrad && p.f32_out ? kSegmentRows / BK : INT_MAX;
+
+    if (warp == 0 && lane == 0) {
+        // ---- producer (both CTAs); the leader's also schedules
+        int it = 0, asks = 0;
+        int tile = (int)(blockIdx.x >> 1);
+        bool asked = false;
+        const auto ask = [&]() {
+            mbar_arrive_expect_tx(clc_bar, 16);
+            clc_try_cancel(clc_resp, clc_bar);
+            asked = true;
+        };
+        // the next tile: -1 when no pending cluster was left to take
+        const auto answer = [&]() {
+            asked = false;
+            // waited for even after an abort, so that it never lands in shared
+            // memory the CTA has left
+            if (!mbar_wait<true>(clc_bar, asks++ & 1)) return -1;
+            const int x = clc_cancelled_cta(clc_resp);
+            if (x < 0) return -1;
+            if ((x & 1) != 0 || x >= (int)gridDim.x) {  // not a cluster's first CTA of this grid
+                *abort_flag = 1;
+                atomicExch(&g_timeout, 1);
+                return -1;
+            }
+            return x >> 1;
+        };
+        for (int k = 0;; ++k) {
+            const int slot = k % kTileSlots;
+            if (leader) {
+                while (tile >= tiles) {  // beyond the last tile: take another cluster
+                    ask();
+                    tile = answer();
+                }
+                if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) {
+                    *abort_flag = 1;
+                    tile = -1;
+                }
+                publish_tile(tile_ids_addr, tile_full0, slot, tile);
+            } else {
+                tile = mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1) ? tile_ids[slot] : -1;
+                mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+            }
+            if (tile < 0) break;
+            const Tile t = tile_at<MODE>(p, groups, tile);
+            const int kblocks = blocks_of(t);
+            const int half = width_of(t) / 2;  // this CTA's rows of the N side
+            const uint32_t bytes = (uint32_t)(A_BYTES + half * BK * 2);
+            const int ask_at = kblocks > kAskAhead ? kblocks - kAskAhead : 0;
+            for (int kb = 0; kb < kblocks && !*abort_flag; ++kb, ++it) {
+                if (leader && kb == ask_at) ask();
+                const int s = it % STAGES;
+                if (!mbar_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
+                uint32_t bar = map_to_rank(full0 + 8 * s, 0);
+                if (MODE == kWgrad) {
+                    if ((kb + 1) * BK > t.rows) {  // rows beyond the group: warp 6 hands the stage on
+                        bar = map_to_rank(tail0 + 8 * s, rank);
+                        mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
+                    } else {
+                        mbar_arrive_expect_tx_cluster(bar, bytes);
+                    }
+                } else if (leader) {
+                    mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+                }
+                if (MODE == kFc1) {
+                    // 32 gate rows and the 32 up rows of the same features, twice
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        tma_load_3d_pair(sa + i * (A_BYTES / 2), &p.a, bar, kb * BK,
+                                         t.m0 + 64 * (int)rank + 32 * i, 2 * t.group);
+                } else if (MODE == kMm) {
+                    tma_load_3d_pair(sa, &p.a, bar, kb * BK, t.m0 + 128 * (int)rank, t.group);
+                } else if (MODE == kDgrad) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        tma_load_3d_pair(sa + i * (A_BYTES / 2), &p.a, bar, t.m0 + 128 * (int)rank + 64 * i, kb * BK,
+                                         t.group);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        tma_load_2d_pair(sa + i * (A_BYTES / 2), &p.a, bar, t.m0 + 128 * (int)rank + 64 * i,
+                                         t.r0 + kb * BK);
+                }
+                if (MODE == kWgrad) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        tma_load_2d_pair(sb + i * (A_BYTES / 2), &p.b[0], bar, t.n0 + 128 * (int)rank + 64 * i,
+                                         t.r0 + kb * BK);
+                } else {
+                    int row = t.r0 + t.n0 + half * (int)rank;
+                    uint32_t dst = sb;
+#pragma unroll
+                    for (int i = 3; i >= 0; --i) {
+                        if (half & (16 << i)) {
+                            tma_load_2d_pair(dst, &p.b[i], bar, kb * BK, row);
+                            row += 16 << i;
+                            dst += (16 << i) * BK * 2;
+                        }
+                    }
+                }
+            }
+            if (leader) {
+                if (!asked && !*abort_flag) ask();
+                tile = asked ? answer() : -1;
+                if (*abort_flag) tile = -1;
+            }
+        }
+        // the leader's full barriers count both CTAs' bytes: once their last
+        // phases complete, every load of the pair has landed
+        if (leader)
+            for (int k = it > STAGES ? it - STAGES : 0; k < it; ++k)
+                mbar_wait(full0 + 8 * (k % STAGES), (k / STAGES) & 1);
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ---- MMA issuer (leader only)
+        int it = 0, lt = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kTileSlots;
+            const int tile = mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1) ? tile_ids[slot] : -1;
+            mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+            if (tile < 0 || *abort_flag) break;
+            const Tile t = tile_at<MODE>(p, groups, tile);
+            const int kblocks = blocks_of(t);
+            const uint32_t idesc = instr_desc(kAMn, kBMn, width_of(t));
+            int kb = 0;
+            do {  // one accumulation
+                const int acc = lt & 1;
+                if (!mbar_wait(acc_empty0 + 8 * acc, ((lt >> 1) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * TILE_N);
+                const int first = kb, last = kblocks - kb > seg_blocks ? kb + seg_blocks : kblocks;
+                for (; kb < last; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    if (!mbar_wait<MODE == kWgrad>(full0 + 8 * s, (it / STAGES) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+                        // K-major: 16 elements along the swizzled row; MN-major: 16
+                        // rows of 128 bytes, 64-element groups A_BYTES / 2 apart
+                        const uint64_t a = kAMn ? smem_desc_128b(sa + kk * UMMA_K * 128, A_BYTES / 2)
+                                                : smem_desc_128b(sa + kk * UMMA_K * 2);
+                        const uint64_t b = kBMn ? smem_desc_128b(sb + kk * UMMA_K * 128, A_BYTES / 2)
+                                                : smem_desc_128b(sb + kk * UMMA_K * 2);
+                        mma_bf16_pair(d, a, b, idesc, (kb != first || kk != 0) ? 1u : 0u);
+                    }
+                    mma_commit_both(empty0 + 8 * s);
+                }
+                if (!ok) break;
+                mma_commit_both(acc_full0 + 8 * acc);
+                ++lt;
+            } while (kb < kblocks);
+            if (!ok) *abort_flag = 1;
+        }
+        mma_commit_local_pair(mma_done);
+        mbar_wait(mma_done, 0);
+    } else if (warp >= 2 && warp < 6) {
+        // ---- epilogue (both CTAs): this CTA's 128 lanes of the accumulator,
+        // a quarter per warp
+        const int quarter = warp & 3;
+        const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
+        float *stg_pair = staging + (quarter >> 1) * (2 * STG_WARP_BYTES / 4);
+        float *stg_warp = staging + quarter * (STG_WARP_BYTES / 4);
+        const int bar_id = 1 + (quarter >> 1);
+        int lt = 0;
+        bool ok = true;
+        // the warp leaves the loop as one: the tile id, the abort flag and the
+        // waits' outcome are warp-uniform
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kTileSlots;
+            int tile = -1;
+            if (lane == 0) {
+                if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1)) tile = tile_ids[slot];
+                mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+            }
+            tile = __shfl_sync(0xffffffffu, tile, 0);
+            // the barriers below need both warps of a pair, so the two leave
+            // together, whichever of them gave up on its wait
+            if (MODE == kFc1 ? any_of_pair(bar_id, tile < 0) : tile < 0) break;
+            const Tile t = tile_at<MODE>(p, groups, tile);
+            const int kblocks = blocks_of(t);
+            const int width = width_of(t);
+            int kb = 0;
+            do {
+                const bool first = kb == 0;
+                kb = kblocks - kb > seg_blocks ? kb + seg_blocks : kblocks;
+                const int acc = lt & 1;
+                // after a wait that ran out the values are undefined, but the warps
+                // stay in step and the accumulator is handed back
+                if (!__all_sync(0xffffffffu, mbar_wait(acc_full0 + 8 * acc, (lt >> 1) & 1))) {
+                    if (lane == 0) *abort_flag = 1;
+                    ok = MODE == kFc1;  // (a pair leaves at the next tile id)
+                }
+                ++lt;
+                tc_fence_after();
+                const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
+#pragma unroll 1
+                for (int c = 0; c < width; c += 32) {
+                    uint32_t v[32];
+                    tmem_load32(tbase + c, v);
+                    tmem_wait_ld();
+                    if (c + 32 >= width) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(acc_empty_leader0 + 8 * acc);
+                    }
+                    if (kblocks == 0) {  // nothing was accumulated
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    }
+                    if constexpr (MODE == kFc1) {
+                        const auto pair_sync = [&]() {
+                            asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
+                        };
+                        pair_sync();  // the previous chunk has been read
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            stg_pair[i * STG_ROW_FC1 + 32 * (quarter & 1) + lane] = __uint_as_float(v[i]);
+                        pair_sync();
+                        // two lanes per row, 16 features each
+                        const int tk = 16 * (quarter & 1) + (lane >> 1), h = lane & 1;
+                        const float *src = stg_pair + tk * STG_ROW_FC1 + 16 * h;
+                        float g[16], u[16];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 a = lds128(src + 4 * i), b = lds128(src + 32 + 4 * i);
+                            g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
+                            u[4 * i] = b.x, u[4 * i + 1] = b.y, u[4 * i + 2] = b.z, u[4 * i + 3] = b.w;
+                        }
+                        const int n = p.features;
+                        const int col = t.m0 + 64 * (int)rank + 32 * (quarter >> 1) + 16 * h;
+                        const bool in = c + tk < t.cnt;
+                        const int live = in ? n - col : 0;
+                        const int64_t row = (int64_t)t.r0 + t.n0 + c + tk;
+                        if (p.q != nullptr) {
+                            // both lanes of the row hold half of its 32-column block
+                            float mg = ckpt8::finite_amax<16>(g), mu = ckpt8::finite_amax<16>(u);
+                            mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, 1));
+                            mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, 1));
+                            const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
+                            uint32_t qg[4], qu[4];
+                            ckpt8::encode<16>(g, ckpt8::encode_factor(cg), qg);
+                            ckpt8::encode<16>(u, ckpt8::encode_factor(cu), qu);
+                            uint8_t *qr = p.q + row * 2 * n + col;
+                            store_codes16(qr, qg, live, n % 16 == 0);
+                            store_codes16(qr + n, qu, live, n % 16 == 0);
+                            if (live > 0 && h == 0) {
+                                const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
+                                uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
+                                sr[0] = (uint8_t)cg;
+                                sr[nb] = (uint8_t)cu;
+                            }
+                        }
+                        if (live > 0) {
+                            const bool wide = n % 16 == 0;
+                            if (p.fc1 != nullptr) {
+                                uint32_t pg[8], pu[8];
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    swiglu::BF16::put2(pg, i, g[i], g[i + 1]);
+                                    swiglu::BF16::put2(pu, i, u[i], u[i + 1]);
+                                }
+                                __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
+                                const bool fw = wide && reinterpret_cast<uintptr_t>(p.fc1) % 32 == 0;
+                                store_bf16x16(fr, pg, live, fw);
+                                store_bf16x16(fr + n, pu, live, fw);
+                            }
+                            float w = 1.0f;
+                            if (p.probs != nullptr && t.group != p.groups) w = p.probs[row];
+                            float gmin = g[0];
+#pragma unroll
+                            for (int i = 1; i < 16; ++i) gmin = fminf(gmin, g[i]);
+                            uint32_t o[8];
+                            if (gmin < -64.0f)
+                                activate16<true>(g, u, w, o);
+                            else
+                                activate16<false>(g, u, w, o);
+                            store_bf16x16(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, o, live,
+                                          wide && reinterpret_cast<uintptr_t>(p.out) % 32 == 0);
+                        }
+                    } else if constexpr (MODE == kWgrad) {
+                        // a lane is a row of dW
+                        const int r = t.m0 + 128 * (int)rank + 32 * quarter + lane;
+                        const int col = t.n0 + c;
+                        if (r < p.features && col < p.cols) {
+                            const int64_t at = ((int64_t)t.group * p.features + r) * p.cols + col;
+                            if (p.f32_out) {
+                                float *o = static_cast<float *>(p.out) + at;
+                                const bool add = p.accumulate || !first;
+#pragma unroll
+                                for (int i = 0; i < 32; i += 8) {
+                                    if (col + i < p.cols) {
+                                        uint32_t w[8];
+#pragma unroll
+                                        for (int x = 0; x < 8; ++x) w[x] = v[i + x];
+                                        if (add) {
+                                            const float4 a = lds128(o + i), b = lds128(o + i + 4);
+                                            const float old[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                                            for (int x = 0; x < 8; ++x)
+                                                w[x] = __float_as_uint(__fadd_rn(old[x], __uint_as_float(w[x])));
+                                        }
+                                        store16(o + i, w[0], w[1], w[2], w[3]);
+                                        store16(o + i + 4, w[4], w[5], w[6], w[7]);
+                                    }
+                                }
+                            } else {
+                                uint32_t w[16];
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2)
+                                    swiglu::BF16::put2(w, i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                                store_row_chunk(static_cast<__nv_bfloat16 *>(p.out) + at, w, col, p.cols,
+                                                p.cols % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0);
+                            }
+                        }
+                    } else {
+                        // transposed through the warp's staging: a lane stores 32
+                        // features of one row
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) stg_warp[i * STG_ROW + lane] = __uint_as_float(v[i]);
+                        __syncwarp();
+                        const int col = t.m0 + 128 * (int)rank + 32 * quarter;
+                        if (c + lane < t.cnt && col < p.features) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 a = lds128(stg_warp + lane * STG_ROW + 4 * i);
+                                swiglu::BF16::put2(w, 4 * i, a.x, a.y);
+                                swiglu::BF16::put2(w, 4 * i + 2, a.z, a.w);
+                            }
+                            const int64_t row = (int64_t)t.r0 + t.n0 + c + lane;
+                            store_row_chunk(static_cast<__nv_bfloat16 *>(p.out) + row * p.features + col, w, col,
+                                            p.features,
+                                            p.features % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0);
+                        }
+                    }
+                }
+            } while (kb < kblocks);
+        }
+    } else if (MODE == kWgrad && warp == 6) {
+        // ---- zero the rows beyond the group in its last stage (both CTAs)
+        int it = 0;
+        uint32_t uses = 0;  // phase of each stage's tail barrier
+        for (int k = 0;; ++k) {
+            const int slot = k % kTileSlots;
+            int tile = -1;
+            if (lane == 0) {
+                if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1)) tile = tile_ids[slot];
+                mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+            }
+            tile = __shfl_sync(0xffffffffu, tile, 0);
+            if (tile < 0) break;
+            const Tile t = tile_at<MODE>(p, groups, tile);
+            it += blocks_of(t);
+            const int live = t.rows % BK;
+            if (live == 0) continue;
+            const int s = (it - 1) % STAGES;
+            if (!__all_sync(0xffffffffu, mbar_wait(tail0 + 8 * s, (uses >> s) & 1))) {
+                if (lane == 0) *abort_flag = 1;
+                break;
+            }
+            uses ^= 1u << s;
+            // four boxes of 64 rows of 128 bytes; the swizzle stays within a row
+            unsigned char *stage = smem + s * STAGE_BYTES;
+            for (int i = lane; i < (BK - live) * 8; i += 32) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    *reinterpret_cast<uint4 *>(stage + b * (A_BYTES / 2) + live * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+            }
+            // the zeros are for the tensor cores (async proxy)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(full0 + 8 * s, 0));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still signal it
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+// A bf16 tensor of `rank` dimensions, innermost first, dense in every row, as
+// boxes of 64 elements of the innermost dimension (128 bytes) with the matching
+// swizzle; zero fill outside.
+bool make_map(EncodeTiled enc, CUtensorMap *map, const void *p, int rank, const int64_t *dims, const int64_t *strides,
+              const int *box) {
+    cuuint64_t d[3], st[2];
+    cuuint32_t bx[3], es[3];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = (cuuint64_t)dims[i];
+        bx[i] = (cuuint32_t)box[i];
+        es[i] = 1;
+    }
+    for (int i = 0; i + 1 < rank; ++i) st[i] = (cuuint64_t)strides[i];
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(p), d, st, bx, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map2(EncodeTiled enc, CUtensorMap *map, const void *p, int64_t inner, int64_t rows, int box_rows) {
+    const int64_t dims[2] = {inner, rows}, strides[1] = {inner * 2};
+    const int box[2] = {BK, box_rows};
+    return make_map(enc, map, p, 2, dims, strides, box);
+}
+
+// W as [outer][rows][inner] with boxes of box_rows x box_outer rows.
+bool map3(EncodeTiled enc, CUtensorMap *map, const void *p, int64_t inner, int64_t rows, int64_t outer, int box_rows,
+          int box_outer) {
+    const int64_t dims[3] = {inner, rows, outer}, strides[2] = {inner * 2, inner * rows * 2};
+    const int box[3] = {BK, box_rows, box_outer};
+    return make_map(enc, map, p, 3, dims, strides, box);
+}
+
+// The N side of the products over rows: boxes of 16, 32, 64 and 128 rows.
+bool row_maps(EncodeTiled enc, CUtensorMap *maps, const void *p, int64_t inner, int64_t rows) {
+    for (int i = 0; i < 4; ++i)
+        if (!map2(enc, maps + i, p, inner, rows, 16 << i)) return false;
+    return true;
+}
+
+template <int MODE>
+swiglu_status_t launch_kernel(const Params &p, int64_t clusters, swiglu_stream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return moe::cuda_fail(e);
+    // the shared-memory opt-in is a per-device function attribute
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (!(dev >= 0 && dev < kMaxDevices && attr_set[dev].load())) {
+        e = cudaFuncSetAttribute(grouped_mm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        if (e != cudaSuccess) return moe::cuda_fail(e);
+        if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true);
+    }
+    e = moe::launch(grouped_mm_kernel<MODE>, dim3((unsigned)(2 * clusters)), MODE == kWgrad ? 224 : 192, SMEM_BYTES,
+                    stream, p);
+    return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
+}
+
+// Clusters of a product over rows: one per tile, at most.  g groups (those
+// that can have a row, the rows of no group counted as one) of c_i rows have
+// sum ceil(c_i / 256) <= (rows + 255 g) / 256 row tiles.
+int64_t most_tiles(int64_t rows, int64_t groups, int64_t features, int tile_f) {
+    const int64_t g = rows < groups + 1 ? rows : groups + 1;
+    return (rows + (TILE_N - 1) * g) / TILE_N * ((features + tile_f - 1) / tile_f);
+}
+
+// The checks that the products share.
+swiglu_status_t check(int64_t rows, int64_t groups, int64_t features, int64_t K, swiglu_dtype_t dtype) {
+    if (dtype != SWIGLU_BF16) return SWIGLU_ERR_DTYPE;
+    if (rows < 0 || rows > INT32_MAX - TILE_N || groups < 1 || groups > kMaxGroups) return SWIGLU_ERR_SHAPE;
+    if (features < 8 || K < 8 || features % 8 != 0 || K % 8 != 0 || K > INT32_MAX / 2 ||
+        features > INT32_MAX / 2 / groups)
+        return SWIGLU_ERR_SHAPE;
+    return SWIGLU_OK;
+}
+
+bool aligned(std::initializer_list<const void *> ps, uintptr_t by) {
+    for (const void *p : ps)
+        if ((uintptr_t)p % by != 0) return false;
+    return true;
+}
+
+}  // namespace gmm
+
+using moe::Span;
+using moe::span_of;
+
+extern "C" {
+
+swiglu_status_t swiglu_grouped_fc1_fwd(const void *x, const void *w, const int32_t *ends, const float *probs, void *y,
+                                       void *fc1, void *q, void *scales, int64_t rows, int64_t groups, int64_t n,
+                                       int64_t K, swiglu_dtype_t dtype, swiglu_stream_t stream) {
+    using namespace gmm;
+    swiglu_status_t st = check(rows, groups, n, K, dtype);
+    if (st == SWIGLU_OK && n > INT32_MAX / 4 / groups) st = SWIGLU_ERR_SHAPE;
+    if (st != SWIGLU_OK || rows == 0) return st;
+    if (x == nullptr || w == nullptr || ends == nullptr || y == nullptr || (q == nullptr) != (scales == nullptr))
+        return SWIGLU_ERR_NULL;
+    if (fc1 != nullptr && q != nullptr) return SWIGLU_ERR_ALIAS;  // one of the two is kept
+    if (!aligned({x, w, y, fc1, q}, 16) || !aligned({ends, probs}, 4)) return SWIGLU_ERR_STRIDE;
+    const int64_t nb = (n + SWIGLU_CKPT8_BLOCK - 1) / SWIGLU_CKPT8_BLOCK;
+    Span sx, sw, se, sp, sy, sf, sq, ss;
+    if (!span_of(x, rows, K, K, 2, sx) || !span_of(w, groups * 2 * n, K, K, 2, sw) ||
+        !span_of(ends, groups, 1, 1, 4, se) || !span_of(probs, rows, 1, 1, 4, sp) || !span_of(y, rows, n, n, 2, sy) ||
+        !span_of(fc1, rows, 2 * n, 2 * n, 2, sf) || !span_of(q, rows, 2 * n, 2 * n, 1, sq) ||
+        !span_of(scales, rows, 2 * nb, 2 * nb, 1, ss))
+        return SWIGLU_ERR_SHAPE;
+    if (moe::any_alias({sy, sf, sq, ss}, {sx, sw, se, sp})) return SWIGLU_ERR_ALIAS;
+    const int64_t clusters = most_tiles(rows, groups, n, kTileF<kFc1>);
+    if (clusters > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
+
+    EncodeTiled enc;
+    const cudaError_t e = encoder(enc);
+    if (e != cudaSuccess) return moe::cuda_fail(e);
+    Params p{};
+    // [gate | up] halves of every expert: 32 rows of each per box
+    if (!map3(enc, &p.a, w, K, n, 2 * groups, 32, 2) || !row_maps(enc, p.b, x, K, rows))
+        return moe::cuda_fail(cudaErrorInvalidValue);
+    p.ends = ends;
+    p.probs = probs;
+    p.out = y;
+    p.fc1 = static_cast<__nv_bfloat16 *>(fc1);
+    p.q = static_cast<uint8_t *>(q);
+    p.scales = static_cast<uint8_t *>(scales);
+    p.rows = (int)rows;
+    p.groups = (int)groups;
+    p.features = (int)n;
+    p.depth = (int)K;
+    return launch_kernel<kFc1>(p, clusters, stream);
+}
+
+swiglu_status_t swiglu_grouped_mm_fwd(const void *x, const void *w, const int32_t *ends, void *y, int64_t rows,
+                                      int64_t groups, int64_t N, int64_t K, swiglu_dtype_t dtype,
+                                      swiglu_stream_t stream) {
+    using namespace gmm;
+    const swiglu_status_t st = check(rows, groups, N, K, dtype);
+    if (st != SWIGLU_OK || rows == 0) return st;
+    if (x == nullptr || w == nullptr || ends == nullptr || y == nullptr) return SWIGLU_ERR_NULL;
+    if (!aligned({x, w, y}, 16) || !aligned({ends}, 4)) return SWIGLU_ERR_STRIDE;
+    Span sx, sw, se, sy;
+    if (!span_of(x, rows, K, K, 2, sx) || !span_of(w, groups * N, K, K, 2, sw) || !span_of(ends, groups, 1, 1, 4, se) ||
+        !span_of(y, rows, N, N, 2, sy))
+        return SWIGLU_ERR_SHAPE;
+    if (moe::any_alias({sy}, {sx, sw, se})) return SWIGLU_ERR_ALIAS;
+    const int64_t clusters = most_tiles(rows, groups, N, kTileF<kMm>);
+    if (clusters > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
+
+    EncodeTiled enc;
+    const cudaError_t e = encoder(enc);
+    if (e != cudaSuccess) return moe::cuda_fail(e);
+    Params p{};
+    if (!map3(enc, &p.a, w, K, N, groups, 128, 1) || !row_maps(enc, p.b, x, K, rows))
+        return moe::cuda_fail(cudaErrorInvalidValue);
+    p.ends = ends;
+    p.out = y;
+    p.rows = (int)rows;
+    p.groups = (int)groups;
+    p.features = (int)N;
+    p.depth = (int)K;
+    return launch_kernel<kMm>(p, clusters, stream);
+}
+
+swiglu_status_t swiglu_grouped_mm_dgrad(const void *dy, const void *w, const int32_t *ends, void *dx, int64_t rows,
+                                        int64_t groups, int64_t N, int64_t K, swiglu_dtype_t dtype,
+                                        swiglu_stream_t stream) {
+    using namespace gmm;
+    const swiglu_status_t st = check(rows, groups, N, K, dtype);
+    if (st != SWIGLU_OK || rows == 0) return st;
+    if (dy == nullptr || w == nullptr || ends == nullptr || dx == nullptr) return SWIGLU_ERR_NULL;
+    if (!aligned({dy, w, dx}, 16) || !aligned({ends}, 4)) return SWIGLU_ERR_STRIDE;
+    Span sdy, sw, se, sdx;
+    if (!span_of(dy, rows, N, N, 2, sdy) || !span_of(w, groups * N, K, K, 2, sw) ||
+        !span_of(ends, groups, 1, 1, 4, se) || !span_of(dx, rows, K, K, 2, sdx))
+        return SWIGLU_ERR_SHAPE;
+    if (moe::any_alias({sdx}, {sdy, sw, se})) return SWIGLU_ERR_ALIAS;
+    const int64_t clusters = most_tiles(rows, groups, K, kTileF<kDgrad>);
+    if (clusters > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
+
+    EncodeTiled enc;
+    const cudaError_t e = encoder(enc);
+    if (e != cudaSuccess) return moe::cuda_fail(e);
+    Params p{};
+    // the contraction runs over W's rows: boxes of 64 columns by 64 of them
+    if (!map3(enc, &p.a, w, K, N, groups, BK, 1) || !row_maps(enc, p.b, dy, N, rows))
+        return moe::cuda_fail(cudaErrorInvalidValue);
+    p.ends = ends;
+    p.out = dx;
+    p.rows = (int)rows;
+    p.groups = (int)groups;
+    p.features = (int)K;
+    p.depth = (int)N;
+    return launch_kernel<kDgrad>(p, clusters, stream);
+}
+
+swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int32_t *ends, void *dw, int64_t rows,
+                                        int64_t groups, int64_t N, int64_t K, swiglu_dtype_t dtype,
+                                        swiglu_dtype_t dw_dtype, int accumulate, swiglu_stream_t stream) {
+    using namespace gmm;
+    const swiglu_status_t st = check(rows, groups, N, K, dtype);
+    if (st != SWIGLU_OK) return st;
+    if (dw_dtype != SWIGLU_BF16 && dw_dtype != SWIGLU_F32) return SWIGLU_ERR_DTYPE;
+    if (accumulate != 0 && dw_dtype != SWIGLU_F32) return SWIGLU_ERR_DTYPE;
+    const int eb = dw_dtype == SWIGLU_F32 ? 4 : 2;
+    Span sdw;
+    if (!span_of(dw, groups * N, K, K, eb, sdw)) return SWIGLU_ERR_SHAPE;
+    if (rows == 0) {  // every group is empty
+        if (accumulate != 0) return SWIGLU_OK;
+        if (dw == nullptr) return SWIGLU_ERR_NULL;
+        if (!aligned({dw}, 16)) return SWIGLU_ERR_STRIDE;
+        const cudaError_t e = cudaMemsetAsync(dw, 0, sdw.hi - sdw.lo, reinterpret_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
+    }
+    if (dy == nullptr || x == nullptr || ends == nullptr || dw == nullptr) return SWIGLU_ERR_NULL;
+    if (!aligned({dy, x, dw}, 16) || !aligned({ends}, 4)) return SWIGLU_ERR_STRIDE;
+    Span sdy, sx, se;
+    if (!span_of(dy, rows, N, N, 2, sdy) || !span_of(x, rows, K, K, 2, sx) || !span_of(ends, groups, 1, 1, 4, se))
+        return SWIGLU_ERR_SHAPE;
+    if (moe::any_alias({sdw}, {sdy, sx, se})) return SWIGLU_ERR_ALIAS;
+    const int64_t clusters = groups * ((N + 255) / 256) * ((K + TILE_N - 1) / TILE_N);
+    if (clusters > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
+
+    EncodeTiled enc;
+    const cudaError_t e = encoder(enc);
+    if (e != cudaSuccess) return moe::cuda_fail(e);
+    Params p{};
+    if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK))
+        return moe::cuda_fail(cudaErrorInvalidValue);
+    p.ends = ends;
+    p.out = dw;
+    p.rows = (int)rows;
+    p.groups = (int)groups;
+    p.features = (int)N;
+    p.cols = (int)K;
+    p.f32_out = dw_dtype == SWIGLU_F32;
+    p.accumulate = accumulate != 0;
+    return launch_kernel<kWgrad>(p, clusters, stream);
+}
+
+swiglu_status_t swiglu_grouped_timeout_flag(int *flag) {
+    if (flag == nullptr) return SWIGLU_ERR_NULL;
+    const cudaError_t e = cudaMemcpyFromSymbol(flag, gmm::g_timeout, sizeof(int));
+    return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
+}
+
+}  // extern "C"
