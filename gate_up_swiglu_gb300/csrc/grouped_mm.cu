@@ -98,11 +98,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return mbar_wait_or_flag<kCluster>(bar, parity, &g_timeout);
 }
 
-// Arrive on a barrier of the cluster, expecting `bytes` more.
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar_cluster, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster),
-                 "r"(bytes)
-                 : "memory");
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 struct Params {
@@ -316,8 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            // kWgrad: each CTA arrives for its own half (the producer, or warp 6
-            // once the rows beyond the group are zero)
+            // kWgrad: an arrival for each CTA's half (both by the leader's producer,
+            // or warp 6 of each once the rows beyond the group are zero)
             mbar_init(full0 + 8 * s, MODE == kWgrad ? 2 : 1);
             mbar_init(empty0 + 8 * s, 1);
             mbar_init(tail0 + 8 * s, 1);
@@ -364,8 +361,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
     // contraction blocks per accumulation (kWgrad with fp32 results: a segment)
     const int seg_blocks = MODE == kWgrad && p.f32_out ? kSegmentRows / BK : INT_MAX;
 
-    if (warp == 0 && lane == 0) {
-        // ---- producer (both CTAs); the leader's also schedules
+    if (warp == 0 && elect_one()) {
+        // ---- producer (both CTAs); the leader's also schedules.  (With the
+        // thread picked by `lane == 0` each load cost ~400 cycles to issue: 8192 x
+        // 4096 x 8192 1390 TFLOP/s with three loads a stage, 740 with four,
+        // against 1875 and 814.)
         int it = 0, asks = 0;
         int tile = (int)(blockIdx.x >> 1);
         bool asked = false;
@@ -420,15 +420,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
                 }
                 const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
                 uint32_t bar = map_to_rank(full0 + 8 * s, 0);
-                if (MODE == kWgrad) {
-                    if ((kb + 1) * BK > t.rows) {  // rows beyond the group: warp 6 hands the stage on
-                        bar = map_to_rank(tail0 + 8 * s, rank);
-                        mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
-                    } else {
-                        mbar_arrive_expect_tx_cluster(bar, bytes);
-                    }
+                if (MODE == kWgrad && (kb + 1) * BK > t.rows) {
+                    // rows beyond the group: warp 6 of each CTA hands its half on
+                    bar = map_to_rank(tail0 + 8 * s, rank);
+                    mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
                 } else if (leader) {
                     mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+                    if (MODE == kWgrad) mbar_arrive(full0 + 8 * s);  // for both halves
                 }
                 if (MODE == kFc1) {
                     // 32 gate rows and the 32 up rows of the same features, twice
@@ -478,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
         if (leader)
             for (int k = it > STAGES ? it - STAGES : 0; k < it; ++k)
                 mbar_wait(full0 + 8 * (k % STAGES), (k / STAGES) & 1);
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader && elect_one()) {
         // ---- MMA issuer (leader only)
         int it = 0, lt = 0;
         bool ok = true;
@@ -502,7 +500,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
                 const int first = kb, last = kblocks - kb > seg_blocks ? kb + seg_blocks : kblocks;
                 for (; kb < last; ++kb, ++it) {
                     const int s = it % STAGES;
-                    if (!mbar_wait<MODE == kWgrad>(full0 + 8 * s, (it / STAGES) & 1)) {
+                    // (a stage whose last rows were zeroed by both CTAs' threads: acquire
+                    // their writes)
+                    const bool zeroed = MODE == kWgrad && (kb + 1) * BK > t.rows;
+                    if (!(zeroed ? mbar_wait<true>(full0 + 8 * s, (it / STAGES) & 1)
+                                 : mbar_wait(full0 + 8 * s, (it / STAGES) & 1))) {
                         ok = false;
                         break;
                     }

@@ -150,6 +150,21 @@ __device__ __forceinline__ void store_row_chunk(__nv_bfloat16 *p, const uint32_t
     }
 }
 
+// True in one lane of a (converged) warp.  A role that issues TMA loads or MMAs
+// from one thread picks it this way: the compiler then knows that a single
+// thread is active and issues them directly.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
