@@ -31,6 +31,9 @@ bool multiple(int64_t by, std::initializer_list<int64_t> v) {
     return true;
 }
 
+// Blocks of 32 columns a warp of the single-element kernels takes at a time.
+constexpr int kNarrowFwd = 8, kNarrowBwd = 4;
+
 // CTAs of T threads for `packs` packs, one pack a thread (the kernels' grid
 // stride covers what the launch limit leaves).
 unsigned one_pass(int64_t packs, int T) {
@@ -41,10 +44,19 @@ unsigned one_pass(int64_t packs, int T) {
 template <typename E, int VEC>
 swiglu_status_t launch_fwd(ckpt8::FwdParams p, swiglu_stream_t stream) {
     constexpr int T = 128;
-    p.row_packs = p.blocks * (ckpt8::kBlock / VEC);
-    p.packs = p.rows * p.row_packs;
-    p.div = make_fast_div((uint64_t)p.row_packs);
-    const cudaError_t e = moe::launch(ckpt8::ckpt8_fwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, p);
+    cudaError_t e;
+    if constexpr (VEC == 1) {
+        constexpr int K = kNarrowFwd;
+        p.row_packs = (int32_t)((p.n + 32 * K - 1) / (32 * K));
+        p.packs = p.rows * p.row_packs;
+        p.div = make_fast_div((uint64_t)p.row_packs);
+        e = moe::launch(ckpt8::ckpt8_fwd_narrow_kernel<E, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, p);
+    } else {
+        p.row_packs = p.blocks * (ckpt8::kBlock / VEC);
+        p.packs = p.rows * p.row_packs;
+        p.div = make_fast_div((uint64_t)p.row_packs);
+        e = moe::launch(ckpt8::ckpt8_fwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, p);
+    }
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
 
@@ -58,6 +70,12 @@ swiglu_status_t launch_bwd(ckpt8::BwdParams p, swiglu_stream_t stream) {
     if (p.dw != nullptr) {
         const unsigned grid = (unsigned)(p.rows < INT32_MAX ? p.rows : INT32_MAX);
         e = moe::launch(ckpt8::ckpt8_bwd_weighted_kernel<E, VEC, T>, dim3(grid), T, 0, stream, p);
+    } else if constexpr (VEC == 1) {
+        constexpr int K = kNarrowBwd;
+        p.row_packs = (int32_t)((p.n + 32 * K - 1) / (32 * K));
+        p.packs = p.rows * p.row_packs;
+        p.div = make_fast_div((uint64_t)p.row_packs);
+        e = moe::launch(ckpt8::ckpt8_bwd_narrow_kernel<E, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, p);
     } else {
         e = moe::launch(ckpt8::ckpt8_bwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, p);
     }

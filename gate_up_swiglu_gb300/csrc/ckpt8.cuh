@@ -96,22 +96,6 @@ __device__ __forceinline__ void decode(const uint32_t *q, float f, float *v) {
     }
 }
 
-// N code bytes of a pack (N = 1, 4, 8 or 16), as words.
-template <int N, int LD>
-__device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t *w) {
-    if constexpr (N == 1)
-        w[0] = *p;
-    else
-        swiglu::Ld<N, LD>::run(p, w);
-}
-template <int N>
-__device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t *w) {
-    if constexpr (N == 1)
-        *p = (uint8_t)w[0];
-    else
-        swiglu::St<N, swiglu::kStStream>::run(p, w);
-}
-
 // ---------------------------------------------------------------- kernels ---
 // Both are one pass over the data: the forward reads x (2 elements a pair) and
 // writes y, two codes and 2/32 scale bytes; the backward reads dy, the codes
@@ -181,8 +165,8 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
         encode<VEC>(g, encode_factor(cg), qg);
         encode<VEC>(u, encode_factor(cu), qu);
         uint8_t *qr = p.q + r * p.q_stride + col;
-        store_codes<VEC>(qr, qg);
-        store_codes<VEC>(qr + p.n, qu);
+        swiglu::St<VEC, swiglu::kStStream>::run(qr, qg);
+        swiglu::St<VEC, swiglu::kStStream>::run(qr + p.n, qu);
         if (c % kLanes == 0) {
             uint8_t *sr = p.scales + r * p.s_stride + c / kLanes;
             sr[0] = (uint8_t)cg;
@@ -196,6 +180,83 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
         uint32_t o[NW] = {};
         swiglu::store_pack<E, VEC>(o, yv);
         swiglu::St<B, swiglu::kStStream>::run(p.y + r * p.y_stride + col * E::kBytes, o);
+    }
+}
+
+// ------------------------------------------------------ single elements ---
+// Odd n, or rows misaligned to one another: every operand moves element by
+// element.  A warp takes K blocks of 32 columns of one row, one lane per column,
+// so a block's maximum is one warp-wide reduction, each lane forms its row
+// pointers once for K elements, and all loads are issued before the first is
+// used.  (One element per thread over the flattened index, with shuffles for the
+// maximum, took 131 us for the forward of [3000, 2 x 5503] fp32 with weights.)
+
+// Positions of a warp: its row and the first column of its lane.
+struct Segment {
+    int64_t row, col;
+};
+
+template <int K>
+__device__ __forceinline__ Segment segment_at(int64_t seg, int32_t chunks, const swiglu::FastDiv &div) {
+    const int64_t r = swiglu::fast_div(seg, div);
+    return {r, (seg - r * chunks) * (32 * K) + (threadIdx.x & 31)};
+}
+
+// Bits of |v|, 0 unless finite: as integers they order like the values.
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+    const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0u;
+}
+
+// p.row_packs: warps (segments of 32 K columns) per row; p.packs: in all.
+template <typename E, int K, int T>
+__global__ void __launch_bounds__(T) ckpt8_fwd_narrow_kernel(const FwdParams p) {
+    swiglu::await_previous_grid();
+    swiglu::allow_next_grid();
+    constexpr int EB = E::kBytes;
+    for (int64_t seg = (int64_t)blockIdx.x * (T / 32) + (threadIdx.x >> 5); seg < p.packs;
+         seg += (int64_t)gridDim.x * (T / 32)) {
+        const Segment at = segment_at<K>(seg, p.row_packs, p.div);
+        const char *xr = p.x + at.row * p.x_stride + at.col * EB;
+        const char *ur = xr + p.n * EB;
+        const int live = (int)min((int64_t)K, (p.n - at.col + 31) / 32);  // elements of this lane (<= 0: none)
+        uint32_t g[K], u[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            g[i] = u[i] = 0u;
+            if (i < live) {
+                swiglu::Ld<EB, swiglu::kLdNC>::run(xr + i * 32 * EB, &g[i]);
+                swiglu::Ld<EB, swiglu::kLdNC>::run(ur + i * 32 * EB, &u[i]);
+            }
+        }
+        const float wr = p.w != nullptr ? __ldg(p.w + at.row) : 1.0f;
+        char *yr = p.y + at.row * p.y_stride + at.col * EB;
+        uint8_t *qr = p.q + at.row * p.q_stride + at.col;
+        uint8_t *sr = p.scales + at.row * p.s_stride + at.col / kBlock;
+        const int64_t first = at.col - (threadIdx.x & 31);
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            if (first + 32 * i >= p.n) break;  // the same for the whole warp
+            const float gf = E::get(&g[i], 0), uf = E::get(&u[i], 0);
+            const uint32_t cg = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, finite_bits(gf))));
+            const uint32_t cu = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, finite_bits(uf))));
+            if (i < live) {
+                uint32_t qg, qu;
+                encode<1>(&gf, encode_factor(cg), &qg);
+                encode<1>(&uf, encode_factor(cu), &qu);
+                qr[i * 32] = (uint8_t)qg;
+                qr[p.n + i * 32] = (uint8_t)qu;
+                const swiglu::Act act = swiglu::activation<E, false, true>(gf);
+                const float y = __fmul_rn(__fmul_rn(__fmul_rn(act.silu, uf), wr), act.scale);
+                uint32_t o = 0u;
+                E::put(&o, 0, y);
+                swiglu::St<EB, swiglu::kStStream>::run(yr + i * 32 * EB, &o);
+            }
+            if ((threadIdx.x & 31) == 0) {
+                sr[i] = (uint8_t)cg;
+                sr[i + p.blocks] = (uint8_t)cu;
+            }
+        }
     }
 }
 
@@ -254,8 +315,8 @@ __device__ __forceinline__ void bwd_one(const BwdParams &p, int64_t r, int32_t c
     const uint8_t *qr = p.q + r * p.q_stride + col;
     const uint8_t *sr = p.scales + r * p.s_stride + col / kBlock;
     swiglu::Ld<B, swiglu::kLdNC>::run(p.dy + r * p.dy_stride + col * E::kBytes, d);
-    load_codes<VEC, swiglu::kLdNC>(qr, qg);
-    load_codes<VEC, swiglu::kLdNC>(qr + p.n, qu);
+    swiglu::Ld<VEC, swiglu::kLdNC>::run(qr, qg);
+    swiglu::Ld<VEC, swiglu::kLdNC>::run(qr + p.n, qu);
     const uint32_t cg = __ldg(sr), cu = __ldg(sr + p.blocks);
     float g[VEC], u[VEC], dg[VEC], du[VEC], yv[VEC];
     decode<VEC>(qg, decode_factor(cg), g);
@@ -292,6 +353,61 @@ __global__ void __launch_bounds__(T) ckpt8_bwd_kernel(const BwdParams p) {
     }
 }
 
+// K elements of one lane (columns col, col + 32, ...), all loads first.
+template <typename E, int K, int MODE>
+__device__ __forceinline__ void bwd_elements(const BwdParams &p, const Segment &at, float wr, float &acc) {
+    constexpr int EB = E::kBytes;
+    const int live = (int)min((int64_t)K, (p.n - at.col + 31) / 32);
+    const char *dyr = p.dy + at.row * p.dy_stride + at.col * EB;
+    const uint8_t *qr = p.q + at.row * p.q_stride + at.col;
+    const uint8_t *ur = qr + p.n;
+    const uint8_t *sr = p.scales + at.row * p.s_stride + at.col / kBlock;
+    uint32_t d[K], qg[K], qu[K], cg[K], cu[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        if (i < live) {
+            swiglu::Ld<EB, swiglu::kLdNC>::run(dyr + i * 32 * EB, &d[i]);
+            qg[i] = qr[i * 32];
+            qu[i] = ur[i * 32];
+            cg[i] = sr[i];
+            cu[i] = sr[i + p.blocks];
+        }
+    }
+    char *dgr = p.dx + at.row * p.dx_stride + at.col * EB;
+    char *dur = dgr + p.n * EB;
+    char *yr = p.y + at.row * p.y_stride + at.col * EB;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        if (i < live) {
+            float g, u, dg, du, y;
+            decode<1>(&qg[i], decode_factor(cg[i]), &g);
+            decode<1>(&qu[i], decode_factor(cu[i]), &u);
+            bwd_values<E, 1, MODE, E::kDeepScale>(&d[i], &g, &u, wr, acc, &dg, &du, &y);
+            uint32_t o = 0u;
+            E::put(&o, 0, dg);
+            swiglu::St<EB, swiglu::kStStream>::run(dgr + i * 32 * EB, &o);
+            o = 0u;
+            E::put(&o, 0, du);
+            swiglu::St<EB, swiglu::kStStream>::run(dur + i * 32 * EB, &o);
+            if (p.y != nullptr) {
+                o = 0u;
+                E::put(&o, 0, y);
+                swiglu::St<EB, swiglu::kStStream>::run(yr + i * 32 * EB, &o);
+            }
+        }
+    }
+}
+
+template <typename E, int K, int T>
+__global__ void __launch_bounds__(T) ckpt8_bwd_narrow_kernel(const BwdParams p) {
+    swiglu::await_previous_grid();
+    swiglu::allow_next_grid();
+    float acc = 0.0f;
+    for (int64_t seg = (int64_t)blockIdx.x * (T / 32) + (threadIdx.x >> 5); seg < p.packs;
+         seg += (int64_t)gridDim.x * (T / 32))
+        bwd_elements<E, K, swiglu::kPlain>(p, segment_at<K>(seg, p.row_packs, p.div), 1.0f, acc);
+}
+
 // With weights: a CTA takes a row, so dw[r] is a sum inside the CTA in a fixed
 // order.
 template <typename E, int VEC, int T>
@@ -302,7 +418,14 @@ __global__ void __launch_bounds__(T) ckpt8_bwd_weighted_kernel(const BwdParams p
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const float wr = __ldg(p.w + r);
         float acc = 0.0f;
-        for (int32_t c = threadIdx.x; c < p.row_packs; c += T) bwd_one<E, VEC, swiglu::kWeight>(p, r, c, wr, acc);
+        if constexpr (VEC == 1) {
+            constexpr int K = 4;
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+            for (int64_t c = warp * (32 * K); c < p.n; c += T * K)
+                bwd_elements<E, K, swiglu::kWeight>(p, {r, c + lane}, wr, acc);
+        } else {
+            for (int32_t c = threadIdx.x; c < p.row_packs; c += T) bwd_one<E, VEC, swiglu::kWeight>(p, r, c, wr, acc);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
         __syncthreads();  // red may still be read for the previous row

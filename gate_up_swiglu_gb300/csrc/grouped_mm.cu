@@ -793,9 +793,10 @@ bool map3(EncodeTiled enc, CUtensorMap *map, const void *p, int64_t inner, int64
     return make_map(enc, map, p, 3, dims, strides, box);
 }
 
-// The N side of the products over rows: boxes of 16, 32, 64 and 128 rows.
+// The N side of the products over rows: boxes of 16, 32, 64 and 128 rows, as far
+// as a CTA's half of a tile of `rows` rows (to 32) can need them.
 bool row_maps(EncodeTiled enc, CUtensorMap *maps, const void *p, int64_t inner, int64_t rows) {
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4 && (i == 0 || 16 << i <= (rows + 31) / 32 * 16); ++i)
         if (!map2(enc, maps + i, p, inner, rows, 16 << i)) return false;
     return true;
 }

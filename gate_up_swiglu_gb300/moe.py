@@ -23,8 +23,7 @@ import ctypes
 
 import torch
 
-from . import (_DTYPE, SWIGLU_BF16, SwigluError, _check_cuda, _on_device, _rows_view, _stream_handle,
-               _vector, lib)
+from . import (_DTYPE, SWIGLU_BF16, SwigluError, _on_device, _raw_stream, _rows_view, _stream_handle, lib)
 
 CKPT8_BLOCK = 32
 MAX_GROUPS = 1024
@@ -53,33 +52,60 @@ def _declare() -> None:
 _declare()
 
 
+_current_device = torch.cuda.current_device
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(name: str, t: torch.Tensor, stream, *args) -> None:
-    with _on_device(t.device):
-        st = getattr(lib, name)(*args, _stream_handle(t, stream))
+def _call(name: str, fn, t: torch.Tensor, stream, *args) -> None:
+    index = t.get_device()
+    if stream is None and index == _current_device():  # the common case, without a context switch
+        st = fn(*args, _raw_stream(index) if _raw_stream is not None else _stream_handle(t, None))
+    else:
+        with _on_device(t.device):
+            st = fn(*args, _stream_handle(t, stream))
     if st != 0:
         raise SwigluError(st, name)
 
 
-def _same_device(t: torch.Tensor, *others) -> None:
-    for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError("all tensors must be on the same CUDA device")
+def _rows(t: torch.Tensor, cols: int, name: str):
+    """(rows, row stride) of a [..., cols] tensor (cols its last dimension)."""
+    if cols and t.is_contiguous():
+        return t.numel() // cols, cols
+    rows, _, stride = _rows_view(t, name)
+    return rows, stride
 
 
-def _ckpt8_views(q, scales, rows, n):
-    """Row strides of the codes and scales of a checkpoint of [rows, 2n]."""
-    nb = -(-n // CKPT8_BLOCK)
-    if q.dtype != Q_DTYPE or scales.dtype != SCALE_DTYPE:
-        raise ValueError("a checkpoint is q (float8_e4m3fn) and scales (float8_e8m0fnu)")
-    qrows, qcols, sq = _rows_view(q, "q")
-    srows, scols, ss = _rows_view(scales, "scales")
-    if (qrows, qcols) != (rows, 2 * n) or (srows, scols) != (rows, 2 * nb):
-        raise ValueError(f"the checkpoint of [{rows}, {2 * n}] is q [{rows}, {2 * n}] and scales [{rows}, {2 * nb}]")
-    return sq, ss
+def _given(t: torch.Tensor, rows: int, cols: int, dtype, device, name: str) -> int:
+    """The row stride of a tensor the caller gave, checked to be [rows, cols]."""
+    if t.device != device:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    r, c, stride = _rows_view(t, name)
+    if (r, c) != (rows, cols):
+        raise ValueError(f"{name} must have {rows} rows of {cols}")
+    return stride
+
+
+def _weights(w: torch.Tensor, rows: int, device, name: str) -> int:
+    """The address of an fp32 vector with one value per row."""
+    if w.dtype != torch.float32 or w.numel() != rows or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {torch.float32} tensor of {rows} elements")
+    if w.device != device:
+        raise ValueError("all tensors must be on the same CUDA device")
+    return w.data_ptr()
+
+
+def _float_type(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("libswiglu operates on CUDA tensors only")
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError("tensors must all be float32 or all bfloat16")
+    return code
 
 
 def swiglu_ckpt8_fwd(x: torch.Tensor, w: torch.Tensor = None, y: torch.Tensor = None, q: torch.Tensor = None,
@@ -87,26 +113,30 @@ def swiglu_ckpt8_fwd(x: torch.Tensor, w: torch.Tensor = None, y: torch.Tensor = 
     """(y, q, scales): y = w[row] * silu(gate) * up and the 8-bit checkpoint of x.
 
     ``w`` (fp32, one weight per row of x) is optional."""
-    if x.shape[-1] % 2:
+    shape, dtype, device = x.shape, x.dtype, x.device
+    two_n = shape[-1]
+    if two_n % 2:
         raise ValueError("x's last dimension must be even (gate and up halves)")
-    lead, n = x.shape[:-1], x.shape[-1] // 2
+    n, lead = two_n // 2, shape[:-1]
+    cols = 2 * ((n + CKPT8_BLOCK - 1) // CKPT8_BLOCK)
+    code = _float_type(x)
+    rows, sx = _rows(x, two_n, "x")
+    sy, sq, ss = n, two_n, cols
     if y is None:
-        y = torch.empty((*lead, n), dtype=x.dtype, device=x.device)
+        y = torch.empty((*lead, n), dtype=dtype, device=device)
+    else:
+        sy = _given(y, rows, n, dtype, device, "y")
     if q is None:
-        q = torch.empty((*lead, 2 * n), dtype=Q_DTYPE, device=x.device)
+        q = torch.empty(shape, dtype=Q_DTYPE, device=device)
+    else:
+        sq = _given(q, rows, two_n, Q_DTYPE, device, "q")
     if scales is None:
-        scales = torch.empty((*lead, 2 * -(-n // CKPT8_BLOCK)), dtype=SCALE_DTYPE, device=x.device)
-    _check_cuda(x, y)
-    _same_device(x, w, q, scales)
-    rows, _, sx = _rows_view(x, "x")
-    yrows, yn, sy = _rows_view(y, "y")
-    if (yrows, yn) != (rows, n):
-        raise ValueError("y must be [..., n] with the rows of x")
-    sq, ss = _ckpt8_views(q, scales, rows, n)
-    if w is not None:
-        _vector(w, "w", rows, torch.float32)
-    _call("swiglu_ckpt8_fwd", x, stream, x.data_ptr(), _ptr(w), y.data_ptr(), q.data_ptr(), scales.data_ptr(), rows,
-          n, sx, sy, sq, ss, _DTYPE[x.dtype])
+        scales = torch.empty((*lead, cols), dtype=SCALE_DTYPE, device=device)
+    else:
+        ss = _given(scales, rows, cols, SCALE_DTYPE, device, "scales")
+    _call("swiglu_ckpt8_fwd", lib.swiglu_ckpt8_fwd, x, stream, x.data_ptr(),
+          None if w is None else _weights(w, rows, device, "w"), y.data_ptr(), q.data_ptr(), scales.data_ptr(), rows, n,
+          sx, sy, sq, ss, code)
     return y, q, scales
 
 
@@ -117,60 +147,69 @@ def swiglu_ckpt8_bwd(dy: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, w:
     fp32 gradient of the row weights (None without ``w``) and, with ``return_y``
     (or a ``y`` given), the forward's output made again from the checkpoint
     (else None)."""
-    lead, n = dy.shape[:-1], dy.shape[-1]
-    if dx is None:
-        dx = torch.empty((*lead, 2 * n), dtype=dy.dtype, device=dy.device)
-    if return_y and y is None:
-        y = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-    if w is not None and dw is None:
-        dw = torch.empty(w.shape, dtype=torch.float32, device=dy.device)
     if w is None and dw is not None:
         raise ValueError("dw is the gradient of w: it needs w")
-    _check_cuda(dy, dx, *([y] if y is not None else []))
-    _same_device(dy, w, dw, q, scales)
-    rows, _, sdy = _rows_view(dy, "dy")
-    dxrows, dxcols, sdx = _rows_view(dx, "dx")
-    if (dxrows, dxcols) != (rows, 2 * n):
-        raise ValueError("dx must be [..., 2n] with the rows of dy")
-    sy = 0
+    shape, dtype, device = dy.shape, dy.dtype, dy.device
+    n = shape[-1]
+    two_n, cols = 2 * n, 2 * ((n + CKPT8_BLOCK - 1) // CKPT8_BLOCK)
+    code = _float_type(dy)
+    rows, sdy = _rows(dy, n, "dy")
+    if q.dtype != Q_DTYPE or scales.dtype != SCALE_DTYPE:
+        raise ValueError("a checkpoint is q (float8_e4m3fn) and scales (float8_e8m0fnu)")
+    if q.device != device or scales.device != device:
+        raise ValueError("all tensors must be on the same CUDA device")
+    (qrows, sq), (srows, ss) = _rows(q, q.shape[-1], "q"), _rows(scales, scales.shape[-1], "scales")
+    if qrows != rows or srows != rows or q.shape[-1] != two_n or scales.shape[-1] != cols:
+        raise ValueError(f"the checkpoint of [{rows}, {two_n}] is q [{rows}, {two_n}] and scales [{rows}, {cols}]")
+    sdx, sy = two_n, n
+    if dx is None:
+        dx = torch.empty((*shape[:-1], two_n), dtype=dtype, device=device)
+    else:
+        sdx = _given(dx, rows, two_n, dtype, device, "dx")
     if y is not None:
-        yrows, yn, sy = _rows_view(y, "y")
-        if (yrows, yn) != (rows, n):
-            raise ValueError("y must have the shape of dy")
-    sq, ss = _ckpt8_views(q, scales, rows, n)
+        sy = _given(y, rows, n, dtype, device, "y")
+    elif return_y:
+        y = torch.empty(shape, dtype=dtype, device=device)
+    wp = dwp = None
     if w is not None:
-        _vector(w, "w", rows, torch.float32)
-        _vector(dw, "dw", rows, torch.float32)
-    _call("swiglu_ckpt8_bwd", dy, stream, dy.data_ptr(), q.data_ptr(), scales.data_ptr(), _ptr(w), dx.data_ptr(),
-          _ptr(dw), _ptr(y), rows, n, sdy, sq, ss, sdx, sy, _DTYPE[dy.dtype])
+        wp = _weights(w, rows, device, "w")
+        if dw is None:
+            dw = torch.empty(w.shape, dtype=torch.float32, device=device)
+            dwp = dw.data_ptr()
+        else:
+            dwp = _weights(dw, rows, device, "dw")
+    _call("swiglu_ckpt8_bwd", lib.swiglu_ckpt8_bwd, dy, stream, dy.data_ptr(), q.data_ptr(), scales.data_ptr(), wp,
+          dx.data_ptr(), dwp, _ptr(y), rows, n, sdy, sq, ss, sdx, sy, code)
     return dx, dw, y
 
 
-def _experts(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, cols: int, what: str):
-    """Checks shared by the products: bf16 x [rows, *] and w [E, N, K], ends [E]."""
-    _check_cuda(x, w)
-    if x.dtype != torch.bfloat16:
+def _rows_and_experts(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, name: str):
+    """Checks shared by the products of rows x [rows, *] with w [E, N, K]."""
+    if not (x.is_cuda and w.is_cuda):
+        raise ValueError("libswiglu operates on CUDA tensors only")
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
         raise ValueError("the grouped products take bfloat16 tensors")
     if x.dim() != 2 or w.dim() != 3:
-        raise ValueError(f"{what} must be [rows, {cols}] and w [experts, N, K]")
-    _ends(ends, x, w.shape[0])
-
-
-def _ends(ends: torch.Tensor, x: torch.Tensor, groups: int) -> None:
-    _vector(ends, "ends", groups, torch.int32)
-    _same_device(x, ends)
-
-
-def _contiguous(*ts) -> None:
-    if not all(t is None or t.is_contiguous() for t in ts):
+        raise ValueError(f"{name} must have two dimensions and w three: [experts, N, K]")
+    if w.device != x.device:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if not (x.is_contiguous() and w.is_contiguous()):
         raise ValueError("the grouped products need contiguous tensors")
+    _check_ends(ends, x, w.shape[0])
+
+
+def _check_ends(ends: torch.Tensor, x: torch.Tensor, groups: int) -> None:
+    if ends.dtype != torch.int32 or ends.numel() != groups or not ends.is_contiguous():
+        raise ValueError(f"ends must be a contiguous {torch.int32} tensor of {groups} elements")
+    if ends.device != x.device:
+        raise ValueError("all tensors must be on the same CUDA device")
 
 
 def _result(t, shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
     if t is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {like.device}")
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {like.device}")
     return t
 
 
@@ -186,7 +225,7 @@ def swiglu_grouped_fc1_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
     8-bit checkpoint."""
     if save not in (None, "bf16", "fp8"):
         raise ValueError('save must be None, "bf16" or "fp8"')
-    _experts(x, w, ends, w.shape[-1], "x")
+    _rows_and_experts(x, w, ends, "x")
     (rows, K), (E, two_n, wk) = x.shape, w.shape
     if wk != K or two_n % 2:
         raise ValueError("w must be [experts, 2n, K] with x's K")
@@ -196,40 +235,35 @@ def swiglu_grouped_fc1_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
     fc1 = _result(fc1, (rows, two_n), x.dtype, x, "fc1") if save == "bf16" else None
     q = _result(q, (rows, two_n), Q_DTYPE, x, "q") if save == "fp8" else None
     scales = _result(scales, (rows, 2 * nb), SCALE_DTYPE, x, "scales") if save == "fp8" else None
-    _contiguous(x, w, y, fc1, q, scales)
-    if probs is not None:
-        _vector(probs, "probs", rows, torch.float32)
-        _same_device(x, probs)
-    _call("swiglu_grouped_fc1_fwd", x, stream, x.data_ptr(), w.data_ptr(), ends.data_ptr(), _ptr(probs), y.data_ptr(),
-          _ptr(fc1), _ptr(q), _ptr(scales), rows, E, n, K, SWIGLU_BF16)
+    _call("swiglu_grouped_fc1_fwd", lib.swiglu_grouped_fc1_fwd, x, stream, x.data_ptr(), w.data_ptr(), ends.data_ptr(),
+          None if probs is None else _weights(probs, rows, x.device, "probs"), y.data_ptr(), _ptr(fc1), _ptr(q),
+          _ptr(scales), rows, E, n, K, SWIGLU_BF16)
     return (y, fc1) if save == "bf16" else (y, q, scales) if save == "fp8" else y
 
 
 def swiglu_grouped_mm_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, y: torch.Tensor = None,
                           stream=None) -> torch.Tensor:
     """y[t] = W[e] x[t]: x [rows, K], w [E, N, K] -> y [rows, N]."""
-    _experts(x, w, ends, w.shape[-1], "x")
+    _rows_and_experts(x, w, ends, "x")
     (rows, K), (E, N, wk) = x.shape, w.shape
     if wk != K:
         raise ValueError("w must be [experts, N, K] with x's K")
     y = _result(y, (rows, N), x.dtype, x, "y")
-    _contiguous(x, w, y)
-    _call("swiglu_grouped_mm_fwd", x, stream, x.data_ptr(), w.data_ptr(), ends.data_ptr(), y.data_ptr(), rows, E, N, K,
-          SWIGLU_BF16)
+    _call("swiglu_grouped_mm_fwd", lib.swiglu_grouped_mm_fwd, x, stream, x.data_ptr(), w.data_ptr(), ends.data_ptr(),
+          y.data_ptr(), rows, E, N, K, SWIGLU_BF16)
     return y
 
 
 def swiglu_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, dx: torch.Tensor = None,
                             stream=None) -> torch.Tensor:
     """dx[t] = W[e]^T dy[t]: dy [rows, N], w [E, N, K] -> dx [rows, K]."""
-    _experts(dy, w, ends, w.shape[1] if w.dim() == 3 else 0, "dy")
+    _rows_and_experts(dy, w, ends, "dy")
     (rows, N), (E, wn, K) = dy.shape, w.shape
     if wn != N:
         raise ValueError("w must be [experts, N, K] with dy's N")
     dx = _result(dx, (rows, K), dy.dtype, dy, "dx")
-    _contiguous(dy, w, dx)
-    _call("swiglu_grouped_mm_dgrad", dy, stream, dy.data_ptr(), w.data_ptr(), ends.data_ptr(), dx.data_ptr(), rows, E,
-          N, K, SWIGLU_BF16)
+    _call("swiglu_grouped_mm_dgrad", lib.swiglu_grouped_mm_dgrad, dy, stream, dy.data_ptr(), w.data_ptr(),
+          ends.data_ptr(), dx.data_ptr(), rows, E, N, K, SWIGLU_BF16)
     return dx
 
 
@@ -238,11 +272,14 @@ def swiglu_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, ends: torch.Tenso
     """dW[e] = sum over the group's rows of dy[t]^T x[t]: dy [rows, N], x [rows, K]
     -> dw [E, N, K] of ``dtype`` (bfloat16, the default, or float32; that of ``dw``
     when one is given).  ``accumulate`` adds to a float32 ``dw``."""
-    _check_cuda(dy, x)
-    if dy.dtype != torch.bfloat16:
+    if not (dy.is_cuda and x.is_cuda):
+        raise ValueError("libswiglu operates on CUDA tensors only")
+    if dy.dtype != torch.bfloat16 or x.dtype != torch.bfloat16:
         raise ValueError("the grouped products take bfloat16 tensors")
-    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
-        raise ValueError("dy must be [rows, N] and x [rows, K] over the same rows")
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or dy.device != x.device:
+        raise ValueError("dy must be [rows, N] and x [rows, K] over the same rows, on one device")
+    if not (dy.is_contiguous() and x.is_contiguous()):
+        raise ValueError("the grouped products need contiguous tensors")
     if dtype is None:
         dtype = dw.dtype if dw is not None else torch.bfloat16
     if dtype not in _DTYPE:
@@ -250,11 +287,10 @@ def swiglu_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, ends: torch.Tenso
     if accumulate and (dw is None or dtype != torch.float32):
         raise ValueError("accumulate adds to a float32 dw: give one")
     (rows, N), K, E = dy.shape, x.shape[1], ends.numel()
-    _ends(ends, dy, E)
+    _check_ends(ends, dy, E)
     dw = _result(dw, (E, N, K), dtype, dy, "dw")
-    _contiguous(dy, x, dw)
-    _call("swiglu_grouped_mm_wgrad", dy, stream, dy.data_ptr(), x.data_ptr(), ends.data_ptr(), dw.data_ptr(), rows, E,
-          N, K, SWIGLU_BF16, _DTYPE[dtype], 1 if accumulate else 0)
+    _call("swiglu_grouped_mm_wgrad", lib.swiglu_grouped_mm_wgrad, dy, stream, dy.data_ptr(), x.data_ptr(),
+          ends.data_ptr(), dw.data_ptr(), rows, E, N, K, SWIGLU_BF16, _DTYPE[dtype], 1 if accumulate else 0)
     return dw
 
 
