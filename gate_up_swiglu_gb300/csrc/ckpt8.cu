@@ -50,12 +50,12 @@ swiglu_status_t launch_fwd(ckpt8::FwdParams p, swiglu_stream_t stream) {
         p.row_packs = (int32_t)((p.n + 32 * K - 1) / (32 * K));
         p.packs = p.rows * p.row_packs;
         p.div = make_fast_div((uint64_t)p.row_packs);
-        e = moe::launch(ckpt8::ckpt8_fwd_narrow_kernel<E, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, p);
+        e = moe::launch(ckpt8::ckpt8_fwd_narrow_kernel<E, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, 0, p);
     } else {
         p.row_packs = p.blocks * (ckpt8::kBlock / VEC);
         p.packs = p.rows * p.row_packs;
         p.div = make_fast_div((uint64_t)p.row_packs);
-        e = moe::launch(ckpt8::ckpt8_fwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, p);
+        e = moe::launch(ckpt8::ckpt8_fwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, 0, p);
     }
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
@@ -69,15 +69,15 @@ swiglu_status_t launch_bwd(ckpt8::BwdParams p, swiglu_stream_t stream) {
     cudaError_t e;
     if (p.dw != nullptr) {
         const unsigned grid = (unsigned)(p.rows < INT32_MAX ? p.rows : INT32_MAX);
-        e = moe::launch(ckpt8::ckpt8_bwd_weighted_kernel<E, VEC, T>, dim3(grid), T, 0, stream, p);
+        e = moe::launch(ckpt8::ckpt8_bwd_weighted_kernel<E, VEC, T>, dim3(grid), T, 0, stream, 0, p);
     } else if constexpr (VEC == 1) {
         constexpr int K = kNarrowBwd;
         p.row_packs = (int32_t)((p.n + 32 * K - 1) / (32 * K));
         p.packs = p.rows * p.row_packs;
         p.div = make_fast_div((uint64_t)p.row_packs);
-        e = moe::launch(ckpt8::ckpt8_bwd_narrow_kernel<E, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, p);
+        e = moe::launch(ckpt8::ckpt8_bwd_narrow_kernel<E, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, 0, p);
     } else {
-        e = moe::launch(ckpt8::ckpt8_bwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, p);
+        e = moe::launch(ckpt8::ckpt8_bwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, 0, p);
     }
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }

@@ -135,13 +135,13 @@ struct Tile {
     int r0, rows;            // the group's rows
 };
 
-// Fill starts and base (one warp).  The last "group" is that of the rows that
-// belong to none.
-template <int MODE>
+// Fill starts and base (one warp) for tiles of TF features by at most TN rows
+// (kWgrad: columns).  The last "group" is that of the rows that belong to none.
+template <int MODE, int TF, int TN>
 __device__ void build_groups(const Params &p, int *starts, int *base) {
     const int lane = threadIdx.x & 31;
-    const int tf = (p.features + kTileF<MODE> - 1) / kTileF<MODE>;
-    const int per_group = MODE == kWgrad ? tf * ((p.cols + TILE_N - 1) / TILE_N) : 0;
+    const int tf = (p.features + TF - 1) / TF;
+    const int per_group = MODE == kWgrad ? tf * ((p.cols + TN - 1) / TN) : 0;
     int end_before = 0, tiles_before = 0;
     for (int e0 = 0; e0 <= p.groups; e0 += 32) {
         const int e = e0 + lane;
@@ -163,7 +163,7 @@ __device__ void build_groups(const Params &p, int *starts, int *base) {
         if (MODE == kWgrad)
             tiles = e < p.groups ? per_group : 0;
         else if (e <= p.groups)
-            tiles = (end - start + TILE_N - 1) / TILE_N * tf;
+            tiles = (end - start + TN - 1) / TN * tf;
         int sum = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -185,7 +185,8 @@ __device__ void build_groups(const Params &p, int *starts, int *base) {
 // Tile order: within a group, blocks of up to kGroupN N tiles; within a block
 // the N tile varies fastest, so a slab of W is read from HBM once per block and
 // the block's rows stay in L2.
-template <int MODE>
+// N tiles of a group are equal, to STEP rows (the last one may be shorter).
+template <int MODE, int TF, int TN, int STEP>
 __device__ __forceinline__ Tile tile_at(const Params &p, const Groups &g, int t) {
     int lo = 0, hi = p.groups;  // the last e with base[e] <= t
     while (lo < hi) {
@@ -200,17 +201,16 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Groups &g, int t)
     o.r0 = g.starts[lo];
     o.rows = g.starts[lo + 1] - o.r0;
     const int extent = MODE == kWgrad ? p.cols : o.rows;
-    const int nt = (extent + TILE_N - 1) / TILE_N;
-    const int tf = (p.features + kTileF<MODE> - 1) / kTileF<MODE>;
+    const int nt = (extent + TN - 1) / TN;
+    const int tf = (p.features + TF - 1) / TF;
     const int local = t - g.base[lo];
     const int block = local / (kGroupN * tf);
     const int first = block * kGroupN;
     const int width = min(kGroupN, nt - first);
     const int in = local - block * (kGroupN * tf);
-    o.m0 = in / width * kTileF<MODE>;
+    o.m0 = in / width * TF;
     const int j = first + in % width;
-    // equal N tiles, to 32 (the last one may be shorter)
-    const int step = MODE == kWgrad ? TILE_N : ((extent + nt - 1) / nt + 31) / 32 * 32;
+    const int step = MODE == kWgrad ? TN : ((extent + nt - 1) / nt + STEP - 1) / STEP * STEP;
     o.n0 = j * step;
     o.cnt = min(step, extent - o.n0);
     return o;
@@ -272,10 +272,10 @@ __device__ __forceinline__ bool any_of_pair(int id, bool v) {
 
 // Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator (bits 4-5 =
 // 1), A and B bf16 (bits 7-9 and 10-12 = 1), A / B MN-major (bits 15, 16), N / 8
-// in bits 17-22, M / 16 in bits 24-28 (M = 256 across the pair).
-__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int n) {
+// in bits 17-22, M / 16 in bits 24-28 (M = 256 across a pair).
+__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int m, int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 template <int MODE>
@@ -342,7 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
     // from here on global memory is read: the previous grid must have completed
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == 2) build_groups<MODE>(p, starts, base);
+    if (warp == 2) build_groups<MODE, kTileF<MODE>, TILE_N>(p, starts, base);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before either signals the other
@@ -406,7 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
                 mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
             }
             if (tile < 0) break;
-            const Tile t = tile_at<MODE>(p, groups, tile);
+            const Tile t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
             const int kblocks = blocks_of(t);
             const int half = width_of(t) / 2;  // this CTA's rows of the N side
             const uint32_t bytes = (uint32_t)(A_BYTES + half * BK * 2);
@@ -485,9 +485,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
             const int tile = mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1) ? tile_ids[slot] : -1;
             mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
             if (tile < 0 || *abort_flag) break;
-            const Tile t = tile_at<MODE>(p, groups, tile);
+            const Tile t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
             const int kblocks = blocks_of(t);
-            const uint32_t idesc = instr_desc(kAMn, kBMn, width_of(t));
+            const uint32_t idesc = instr_desc(kAMn, kBMn, 256, width_of(t));
             int kb = 0;
             do {  // one accumulation
                 const int acc = lt & 1;
@@ -553,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
             // the barriers below need both warps of a pair, so the two leave
             // together, whichever of them gave up on its wait
             if (MODE == kFc1 ? any_of_pair(bar_id, tile < 0) : tile < 0) break;
-            const Tile t = tile_at<MODE>(p, groups, tile);
+            const Tile t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
             const int kblocks = blocks_of(t);
             const int width = width_of(t);
             int kb = 0;
@@ -727,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
             }
             tile = __shfl_sync(0xffffffffu, tile, 0);
             if (tile < 0) break;
-            const Tile t = tile_at<MODE>(p, groups, tile);
+            const Tile t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
             it += blocks_of(t);
             const int live = t.rows % BK;
             if (live == 0) continue;
@@ -756,6 +756,271 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+// ------------------------------------------------- few tiles: split the depth ---
+// When a call has fewer tiles than the GPU has pairs of SMs (a few rows, or a
+// narrow product over many), its time is that of one tile's loads.  Then a
+// cluster of S CTAs (1, 2, 4 or 8), each on its own (cta_group::1), takes a tile
+// of 128 accumulator lanes by at most NT rows and each CTA a slice of the
+// contraction.  The partial sums meet in shared memory: every CTA leaves its own
+// as [row][lane] fp32 over its (by then idle) ring, and CTA r adds up all S of
+// every S-th row, in rank order, and stores them.  The order is fixed, and
+// nothing passes through global memory.  One tile per cluster, no tile
+// scheduling; shared memory is held to half an SM, so that the next launch's
+// CTAs can set up beside this one's last.
+constexpr int kSplitThreads = 192;
+template <int NT>
+constexpr int kSplitStageBytes = A_BYTES + NT * BK * 2;
+template <int NT>
+constexpr int kSplitStages = NT == 32 ? 5 : 3;
+constexpr int kPartialRow = 132;  // fp32 lanes of a row of partial sums, padded
+template <int NT>
+constexpr int kSplitRing = kSplitStages<NT> * kSplitStageBytes<NT>;
+static_assert(kSplitRing<32> >= 32 * kPartialRow * 4 && kSplitRing<128> >= 128 * kPartialRow * 4,
+              "the partial sums fit the ring");
+template <int NT>
+constexpr int kSplitSmem = kSplitRing<NT> + STATE_BYTES + (TABLE_BYTES + 15) / 16 * 16 + 1024;
+static_assert(kSplitSmem<32> <= 113 * 1024 && kSplitSmem<128> <= 113 * 1024, "two CTAs per SM");
+
+// Features of a tile (kFc1: a gate and an up lane for each).
+template <int MODE>
+constexpr int kSplitF = MODE == kFc1 ? 64 : 128;
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
+template <int MODE, int NT>
+__global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(const __grid_constant__ Params p) {
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    unsigned char *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t ring = smem_addr(smem);
+    unsigned char *state = smem + kSplitRing<NT>;
+    const uint32_t st0 = smem_addr(state);
+    constexpr int kStages = kSplitStages<NT>;
+    constexpr int kStage = kSplitStageBytes<NT>;
+    const uint32_t full0 = st0, empty0 = st0 + 8 * kStages, acc_full = st0 + 16 * kStages;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + 16 * kStages + 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(state + 16 * kStages + 12);
+    static_assert(16 * kStages + 16 <= STATE_BYTES, "barriers and state fit their region");
+    int *starts = reinterpret_cast<int *>(state + STATE_BYTES);
+    int *base = starts + kMaxGroups + 2;
+    constexpr bool kAMn = MODE == kDgrad;
+
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(acc_full, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b[0])) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(NT)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 2) build_groups<MODE, kSplitF<MODE>, NT>(p, starts, base);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Groups groups = {starts, base};
+    const int tile = (int)(blockIdx.x / size);
+    const bool live = tile < base[p.groups + 1];  // the same in the whole cluster
+    Tile t = {};
+    int kb0 = 0, kb1 = 0;
+    if (live) {
+        t = tile_at<MODE, kSplitF<MODE>, NT, 16>(p, groups, tile);
+        if (t.group != p.groups) {
+            const int kblocks = (p.depth + BK - 1) / BK;
+            kb0 = (int)((int64_t)kblocks * rank / size);
+            kb1 = (int)((int64_t)kblocks * (rank + 1) / size);
+        }
+    }
+    const int width = (t.cnt + 15) / 16 * 16;
+    if (warp == 0 && elect_one()) {
+        const uint32_t bytes = (uint32_t)(A_BYTES + width * BK * 2);
+        for (int kb = kb0, it = 0; kb < kb1 && !*abort_flag; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait(empty0 + 8 * s, ((it / kStages) & 1) ^ 1)) {
+                *abort_flag = 1;
+                break;
+            }
+            const uint32_t sa = ring + s * kStage, bar = full0 + 8 * s;
+            mbar_arrive_expect_tx(bar, bytes);
+            if (MODE == kFc1) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    tma_load_3d(sa + i * (A_BYTES / 2), &p.a, bar, kb * BK, t.m0 + 32 * i, 2 * t.group);
+            } else if (MODE == kMm) {
+                tma_load_3d(sa, &p.a, bar, kb * BK, t.m0, t.group);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    tma_load_3d(sa + i * (A_BYTES / 2), &p.a, bar, t.m0 + 64 * i, kb * BK, t.group);
+            }
+            int row = t.r0 + t.n0;
+            uint32_t dst = sa + A_BYTES;
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                if ((16 << i) <= NT && (width & (16 << i))) {
+                    tma_load_2d(dst, &p.b[i], bar, kb * BK, row);
+                    row += 16 << i;
+                    dst += (16 << i) * BK * 2;
+                }
+            }
+        }
+    } else if (warp == 1 && kb1 > kb0 && elect_one()) {
+        const uint32_t idesc = instr_desc(kAMn, false, 128, width);
+        for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait(full0 + 8 * s, (it / kStages) & 1)) {
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t sa = ring + s * kStage, sb = sa + A_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+                const uint64_t a = kAMn ? smem_desc_128b(sa + kk * UMMA_K * 128, A_BYTES / 2)
+                                        : smem_desc_128b(sa + kk * UMMA_K * 2);
+                mma_bf16(tmem, a, smem_desc_128b(sb + kk * UMMA_K * 2), idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
+            }
+            mma_commit(empty0 + 8 * s);
+        }
+        mma_commit(acc_full);
+    } else if (warp >= 2 && kb1 > kb0) {
+        // this CTA's partial sums, from tensor memory to [row][lane]; every load
+        // of the ring has been consumed by then
+        const int quarter = warp & 3;
+        float *part = reinterpret_cast<float *>(smem);
+        if (!__all_sync(0xffffffffu, mbar_wait(acc_full, 0)) && lane == 0) *abort_flag = 1;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < width; c += 32) {
+            uint32_t v[32];
+            tmem_load32(tmem + ((uint32_t)(32 * quarter) << 16) + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i < width) part[(c + i) * kPartialRow + 32 * quarter + lane] = __uint_as_float(v[i]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (size > 1) cluster_sync();
+    if (live) {
+        // rows rank, rank + S, ... of the tile: 16 (kFc1) or 32 threads a row, four
+        // features each, summed over the slices in rank order
+        constexpr int kRowThreads = kSplitF<MODE> / 4;
+        const int slices = t.group == p.groups ? 0 : (int)size;
+        const uint32_t part0 = ring;
+        const int f = (int)threadIdx.x % kRowThreads;  // (kSplitThreads is a multiple of kRowThreads)
+        // kFc1: 32 gates, 32 ups, 32 gates, 32 ups
+        const int lane0 = MODE == kFc1 ? f / 8 * 64 + f % 8 * 4 : f * 4;
+        const int col = t.m0 + 4 * f;
+        for (int r0 = (int)rank; r0 < t.cnt; r0 += (int)size * (kSplitThreads / kRowThreads)) {
+            // the same trip count for a whole warp: the block maximum is shuffled
+            const int r = r0 + (int)(threadIdx.x / kRowThreads) * (int)size;
+            const bool in = r < t.cnt && col < p.features;
+            float g[4] = {}, u[4] = {};
+            if (in) {
+                for (int s = 0; s < slices; ++s) {
+                    const uint32_t at = map_to_rank(part0 + (uint32_t)(r * kPartialRow + lane0) * 4, (uint32_t)s);
+                    const float4 a = ld_cluster(at);
+                    g[0] = __fadd_rn(g[0], a.x), g[1] = __fadd_rn(g[1], a.y);
+                    g[2] = __fadd_rn(g[2], a.z), g[3] = __fadd_rn(g[3], a.w);
+                    if (MODE == kFc1) {
+                        const float4 b = ld_cluster(at + 32 * 4);
+                        u[0] = __fadd_rn(u[0], b.x), u[1] = __fadd_rn(u[1], b.y);
+                        u[2] = __fadd_rn(u[2], b.z), u[3] = __fadd_rn(u[3], b.w);
+                    }
+                }
+            }
+            const int64_t row = (int64_t)t.r0 + t.n0 + r;
+            const auto pack = [](const float (&v)[4], uint32_t (&w)[2]) {
+                swiglu::BF16::put2(w, 0, v[0], v[1]);
+                swiglu::BF16::put2(w, 2, v[2], v[3]);
+            };
+            using St8 = swiglu::St<8, swiglu::kStStream>;
+            if constexpr (MODE == kFc1) {
+                const int n = p.features;
+                if (p.q != nullptr) {
+                    float mg = ckpt8::finite_amax<4>(g), mu = ckpt8::finite_amax<4>(u);
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) {  // eight threads hold a block
+                        mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+                        mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+                    }
+                    if (in) {
+                        const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
+                        uint32_t qg, qu;
+                        ckpt8::encode<4>(g, ckpt8::encode_factor(cg), &qg);
+                        ckpt8::encode<4>(u, ckpt8::encode_factor(cu), &qu);
+                        uint8_t *qr = p.q + row * 2 * n + col;
+                        swiglu::St<4, swiglu::kStStream>::run(qr, &qg);
+                        swiglu::St<4, swiglu::kStStream>::run(qr + n, &qu);
+                        if (f % 8 == 0) {
+                            const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
+                            uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
+                            sr[0] = (uint8_t)cg;
+                            sr[nb] = (uint8_t)cu;
+                        }
+                    }
+                }
+                if (in) {
+                    uint32_t w[2];
+                    if (p.fc1 != nullptr) {
+                        __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
+                        pack(g, w);
+                        St8::run(fr, w);
+                        pack(u, w);
+                        St8::run(fr + n, w);
+                    }
+                    const float wr = p.probs != nullptr && t.group != p.groups ? p.probs[row] : 1.0f;
+                    float y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const swiglu::Act act = swiglu::activation<swiglu::BF16, false, true>(g[i]);
+                        y[i] = __fmul_rn(__fmul_rn(__fmul_rn(act.silu, u[i]), wr), act.scale);
+                    }
+                    pack(y, w);
+                    St8::run(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, w);
+                }
+            } else if (in) {
+                uint32_t w[2];
+                pack(g, w);
+                St8::run(static_cast<__nv_bfloat16 *>(p.out) + row * p.features + col, w);
+            }
+        }
+    }
+    if (size > 1) cluster_sync();  // no CTA leaves while another may still read its sums
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NT) : "memory");
     }
 }
 
@@ -794,9 +1059,10 @@ bool map3(EncodeTiled enc, CUtensorMap *map, const void *p, int64_t inner, int64
 }
 
 // The N side of the products over rows: boxes of 16, 32, 64 and 128 rows, as far
-// as a CTA's half of a tile of `rows` rows (to 32) can need them.
+// as a tile of `rows` rows (to 16) can need them; a CTA of a pair loads half of
+// its tile (to 32), which is no more.
 bool row_maps(EncodeTiled enc, CUtensorMap *maps, const void *p, int64_t inner, int64_t rows) {
-    for (int i = 0; i < 4 && (i == 0 || 16 << i <= (rows + 31) / 32 * 16); ++i)
+    for (int i = 0; i < 4 && (i == 0 || 16 << i <= (rows + 15) / 16 * 16); ++i)
         if (!map2(enc, maps + i, p, inner, rows, 16 << i)) return false;
     return true;
 }
@@ -815,16 +1081,53 @@ swiglu_status_t launch_kernel(const Params &p, int64_t clusters, swiglu_stream_t
         if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true);
     }
     e = moe::launch(grouped_mm_kernel<MODE>, dim3((unsigned)(2 * clusters)), MODE == kWgrad ? 224 : 192, SMEM_BYTES,
-                    stream, p);
+                    stream, 0, p);
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
 
-// Clusters of a product over rows: one per tile, at most.  g groups (those
-// that can have a row, the rows of no group counted as one) of c_i rows have
-// sum ceil(c_i / 256) <= (rows + 255 g) / 256 row tiles.
-int64_t most_tiles(int64_t rows, int64_t groups, int64_t features, int tile_f) {
+// Tiles of a product over rows, at most.  g groups (those that can have a row,
+// the rows of no group counted as one) of c_i rows have
+// sum ceil(c_i / tn) <= (rows + (tn - 1) g) / tn row tiles.
+int64_t most_tiles(int64_t rows, int64_t groups, int64_t features, int tile_f, int tn) {
     const int64_t g = rows < groups + 1 ? rows : groups + 1;
-    return (rows + (TILE_N - 1) * g) / TILE_N * ((features + tile_f - 1) / tile_f);
+    return (rows + (tn - 1) * g) / tn * ((features + tile_f - 1) / tile_f);
+}
+
+template <int MODE, int NT>
+swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_stream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return moe::cuda_fail(e);
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (!(dev >= 0 && dev < kMaxDevices && attr_set[dev].load())) {
+        e = cudaFuncSetAttribute(grouped_mm_split_kernel<MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSplitSmem<NT>);
+        if (e != cudaSuccess) return moe::cuda_fail(e);
+        if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true);
+    }
+    e = moe::launch(grouped_mm_split_kernel<MODE, NT>, dim3((unsigned)(tiles * size)), kSplitThreads, kSplitSmem<NT>,
+                    stream, size, p);
+    return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
+}
+
+// Launch a product over rows.  Pairs of CTAs while there are tiles for at least
+// kPairsWanted of them; below that the split kernel, with as many CTAs per tile
+// as keep the grid within two per SM (and two blocks of depth per CTA at least).
+constexpr int64_t kPairsWanted = 76;
+constexpr int64_t kSplitCtas = 304;
+
+template <int MODE>
+swiglu_status_t launch_rows(const Params &p, swiglu_stream_t stream) {
+    const int64_t pairs = most_tiles(p.rows, p.groups, p.features, kTileF<MODE>, TILE_N);
+    if (pairs > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
+    if (pairs >= kPairsWanted) return launch_kernel<MODE>(p, pairs, stream);
+    const bool few = p.rows <= 32;
+    const int64_t tiles = most_tiles(p.rows, p.groups, p.features, kSplitF<MODE>, few ? 32 : 128);
+    const int kblocks = (p.depth + BK - 1) / BK;
+    int size = 1;
+    while (size < 8 && tiles * size * 2 <= kSplitCtas && size * 4 <= kblocks) size *= 2;
+    return few ? launch_split<MODE, 32>(p, tiles, size, stream) : launch_split<MODE, 128>(p, tiles, size, stream);
 }
 
 // The checks that the products share.
@@ -869,8 +1172,6 @@ swiglu_status_t swiglu_grouped_fc1_fwd(const void *x, const void *w, const int32
         !span_of(scales, rows, 2 * nb, 2 * nb, 1, ss))
         return SWIGLU_ERR_SHAPE;
     if (moe::any_alias({sy, sf, sq, ss}, {sx, sw, se, sp})) return SWIGLU_ERR_ALIAS;
-    const int64_t clusters = most_tiles(rows, groups, n, kTileF<kFc1>);
-    if (clusters > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
 
     EncodeTiled enc;
     const cudaError_t e = encoder(enc);
@@ -889,7 +1190,7 @@ swiglu_status_t swiglu_grouped_fc1_fwd(const void *x, const void *w, const int32
     p.groups = (int)groups;
     p.features = (int)n;
     p.depth = (int)K;
-    return launch_kernel<kFc1>(p, clusters, stream);
+    return launch_rows<kFc1>(p, stream);
 }
 
 swiglu_status_t swiglu_grouped_mm_fwd(const void *x, const void *w, const int32_t *ends, void *y, int64_t rows,
@@ -905,8 +1206,6 @@ swiglu_status_t swiglu_grouped_mm_fwd(const void *x, const void *w, const int32_
         !span_of(y, rows, N, N, 2, sy))
         return SWIGLU_ERR_SHAPE;
     if (moe::any_alias({sy}, {sx, sw, se})) return SWIGLU_ERR_ALIAS;
-    const int64_t clusters = most_tiles(rows, groups, N, kTileF<kMm>);
-    if (clusters > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
 
     EncodeTiled enc;
     const cudaError_t e = encoder(enc);
@@ -920,7 +1219,7 @@ swiglu_status_t swiglu_grouped_mm_fwd(const void *x, const void *w, const int32_
     p.groups = (int)groups;
     p.features = (int)N;
     p.depth = (int)K;
-    return launch_kernel<kMm>(p, clusters, stream);
+    return launch_rows<kMm>(p, stream);
 }
 
 swiglu_status_t swiglu_grouped_mm_dgrad(const void *dy, const void *w, const int32_t *ends, void *dx, int64_t rows,
@@ -936,8 +1235,6 @@ swiglu_status_t swiglu_grouped_mm_dgrad(const void *dy, const void *w, const int
         !span_of(ends, groups, 1, 1, 4, se) || !span_of(dx, rows, K, K, 2, sdx))
         return SWIGLU_ERR_SHAPE;
     if (moe::any_alias({sdx}, {sdy, sw, se})) return SWIGLU_ERR_ALIAS;
-    const int64_t clusters = most_tiles(rows, groups, K, kTileF<kDgrad>);
-    if (clusters > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
 
     EncodeTiled enc;
     const cudaError_t e = encoder(enc);
@@ -952,7 +1249,7 @@ swiglu_status_t swiglu_grouped_mm_dgrad(const void *dy, const void *w, const int
     p.groups = (int)groups;
     p.features = (int)K;
     p.depth = (int)N;
-    return launch_kernel<kDgrad>(p, clusters, stream);
+    return launch_rows<kDgrad>(p, stream);
 }
 
 swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int32_t *ends, void *dw, int64_t rows,

@@ -52,20 +52,24 @@ inline bool any_alias(std::initializer_list<Span> outs, std::initializer_list<Sp
 
 // Launch with programmatic stream serialization: the kernel may launch while
 // the previous kernel in the stream finishes, and waits for that kernel's
-// completion itself before its first global memory access.
+// completion itself before its first global memory access.  cluster > 0: in
+// clusters of that many CTAs (0: as the kernel is declared).
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem, swiglu_stream_t stream,
-                   Args &&...args) {
+                   int cluster, Args &&...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 

@@ -46,7 +46,8 @@ def _ends(counts):
 # (rows per expert, rows of no expert)
 GROUPS = [([1], 0), ([0, 1], 0), ([1, 0, 0, 1], 1), ([0, 0], 3), ([31, 32, 33], 0), ([63, 64, 65], 2),
           ([255, 0, 256, 257], 0), ([300, 1, 513, 0, 7], 40), ([5] * 40, 0), ([1100, 20], 0)]
-WIDTHS = [(8, 8), (64, 64), (136, 72), (256, 200), (264, 520)]
+# the widest give enough tiles for the kernel of CTA pairs, the others split the depth
+WIDTHS = [(8, 8), (64, 64), (136, 72), (256, 200), (264, 520), (4104, 72), (72, 4104), (2056, 2176)]
 
 
 def _same_bits(a, b):
@@ -75,7 +76,8 @@ def test_products_exact_on_integers(sw, counts, tail, N, K):
 
 
 @pytest.mark.parametrize("counts,tail", GROUPS)
-@pytest.mark.parametrize("n,K", [(8, 8), (24, 64), (72, 136), (128, 64), (200, 264), (160, 72)])
+@pytest.mark.parametrize("n,K", [(8, 8), (24, 64), (72, 136), (128, 64), (200, 264), (160, 72), (2056, 136),
+                                 (40, 2056)])
 @pytest.mark.parametrize("probs", [False, True])
 def test_first_product_exact_on_integers(sw, counts, tail, n, K, probs):
     """fc1 and its checkpoint bit for bit, y within one bf16 step."""
