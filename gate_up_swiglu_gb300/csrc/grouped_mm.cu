@@ -81,14 +81,17 @@ constexpr int OFF_TMEM = OFF_TILE_ID + 4 * kTileSlots;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
 constexpr int STATE_BYTES = 512;
 static_assert(OFF_ABORT + 4 <= STATE_BYTES, "barriers and state fit their region");
-// the epilogue's staging: 32 rows of 32 features per warp, or of 32 gates and
-// 32 ups per pair of warps (kFc1), fp32, rows padded by 4 words
-constexpr int STG_ROW = 36, STG_ROW_FC1 = 68;
-constexpr int STG_WARP_BYTES = 32 * STG_ROW * 4;
+// the epilogue's staging, per warp: buffers of 32 rows of 64 bytes for bulk
+// stores (64-byte swizzle); kFc1: 32 rows of 32 gates and 32 ups per pair of
+// warps, fp32, rows padded by 4 words
+constexpr int kBuffers = 3;
+constexpr int BUF_BYTES = 32 * 64;
+constexpr int STG_WARP_BYTES = kBuffers * BUF_BYTES;
 constexpr int STG_BYTES = 4 * STG_WARP_BYTES;
+constexpr int STG_ROW_FC1 = 68;
 static_assert(32 * STG_ROW_FC1 * 4 <= 2 * STG_WARP_BYTES, "a pair of warps has the room of two");
 constexpr int TABLE_BYTES = 2 * (kMaxGroups + 2) * 4;
-constexpr int SMEM_BYTES = RING_BYTES + STATE_BYTES + STG_BYTES + (TABLE_BYTES + 15) / 16 * 16 + 1024;
+constexpr int SMEM_BYTES = RING_BYTES + STG_BYTES + STATE_BYTES + (TABLE_BYTES + 15) / 16 * 16 + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM");
 
 __device__ int g_timeout = 0;
@@ -105,6 +108,7 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 struct Params {
     CUtensorMap a;     // the M side
     CUtensorMap b[4];  // the N side, boxes of 16, 32, 64 and 128 rows (kWgrad: b[0] alone, 64 rows)
+    CUtensorMap c;     // the result (not kFc1), boxes of 64 bytes by 32 rows
     const int32_t *ends;
     const float *probs;      // kFc1
     void *out;               // y, dx or dW
@@ -285,7 +289,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t ring = smem_addr(smem);
-    unsigned char *state = smem + RING_BYTES;
+    unsigned char *staging = smem + RING_BYTES;
+    unsigned char *state = staging + STG_BYTES;
     const uint32_t st0 = smem_addr(state);
     const uint32_t full0 = st0 + OFF_FULL, empty0 = st0 + OFF_EMPTY, tail0 = st0 + OFF_TAIL;
     const uint32_t acc_full0 = st0 + OFF_ACC_FULL, acc_empty0 = st0 + OFF_ACC_EMPTY;
@@ -296,8 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
     volatile int *tile_ids = reinterpret_cast<volatile int *>(state + OFF_TILE_ID);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(state + OFF_ABORT);
-    float *staging = reinterpret_cast<float *>(state + STATE_BYTES);
-    int *starts = reinterpret_cast<int *>(state + STATE_BYTES + STG_BYTES);
+    int *starts = reinterpret_cast<int *>(state + STATE_BYTES);
     int *base = starts + kMaxGroups + 2;
 
     constexpr bool kAMn = MODE == kDgrad || MODE == kWgrad;
@@ -535,8 +539,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
         // a quarter per warp
         const int quarter = warp & 3;
         const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
-        float *stg_pair = staging + (quarter >> 1) * (2 * STG_WARP_BYTES / 4);
-        float *stg_warp = staging + quarter * (STG_WARP_BYTES / 4);
+        float *stg_pair = reinterpret_cast<float *>(staging + (quarter >> 1) * (2 * STG_WARP_BYTES));
+        unsigned char *buffers = staging + quarter * STG_WARP_BYTES;
+        int buf = 0;
+        // the next buffer, once the bulk store that read it last is done with it
+        const auto next_buffer = [&]() {
+            buf = buf == kBuffers - 1 ? 0 : buf + 1;
+            if (elect_one()) bulk_wait_read<kBuffers - 1>();
+            __syncwarp();
+            return buffers + buf * BUF_BYTES;
+        };
         const int bar_id = 1 + (quarter >> 1);
         int lt = 0;
         bool ok = true;
@@ -560,6 +572,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
             do {
                 const bool first = kb == 0;
                 kb = kblocks - kb > seg_blocks ? kb + seg_blocks : kblocks;
+                // a later segment adds to what the one before it has written
+                if (MODE == kWgrad && !first && elect_one()) bulk_wait<0>();
                 const int acc = lt & 1;
                 // after a wait that ran out the values are undefined, but the warps
                 // stay in step and the accumulator is handed back
@@ -573,8 +587,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
 #pragma unroll 1
                 for (int c = 0; c < width; c += 32) {
                     uint32_t v[32];
-                    tmem_load32(tbase + c, v);
-                    tmem_wait_ld();
+                    if constexpr (MODE == kMm || MODE == kDgrad) {
+                        uint32_t lo[16], hi[16];  // lanes 0 - 15 and 16 - 31 of the quarter
+                        tmem_load_16x32(tbase + c, lo);
+                        tmem_load_16x32(tbase + (16u << 16) + c, hi);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = lo[i], v[16 + i] = hi[i];
+                    } else {
+                        tmem_load32(tbase + c, v);
+                        tmem_wait_ld();
+                    }
                     if (c + 32 >= width) {
                         tc_fence_before();
                         __syncwarp();
@@ -655,65 +678,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
                                           wide && reinterpret_cast<uintptr_t>(p.out) % 32 == 0);
                         }
                     } else if constexpr (MODE == kWgrad) {
-                        // a lane is a row of dW
-                        const int r = t.m0 + 128 * (int)rank + 32 * quarter + lane;
-                        const int col = t.n0 + c;
-                        if (r < p.features && col < p.cols) {
-                            const int64_t at = ((int64_t)t.group * p.features + r) * p.cols + col;
-                            if (p.f32_out) {
-                                float *o = static_cast<float *>(p.out) + at;
-                                const bool add = p.accumulate || !first;
+                        // a lane is a row of dW; stores beyond its rows and columns
+                        // are cut off by the tensor map
+                        const int row0 = t.m0 + 128 * (int)rank + 32 * quarter;
+                        const int swz = (lane >> 1) & 3;
+                        if (p.f32_out) {
+                            const bool add = p.accumulate || !first;
 #pragma unroll
-                                for (int i = 0; i < 32; i += 8) {
-                                    if (col + i < p.cols) {
-                                        uint32_t w[8];
+                            for (int h = 0; h < 2; ++h) {
+                                unsigned char *to = next_buffer();
 #pragma unroll
-                                        for (int x = 0; x < 8; ++x) w[x] = v[i + x];
-                                        if (add) {
-                                            const float4 a = lds128(o + i), b = lds128(o + i + 4);
-                                            const float old[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                                            for (int x = 0; x < 8; ++x)
-                                                w[x] = __float_as_uint(__fadd_rn(old[x], __uint_as_float(w[x])));
-                                        }
-                                        store16(o + i, w[0], w[1], w[2], w[3]);
-                                        store16(o + i + 4, w[4], w[5], w[6], w[7]);
-                                    }
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<uint4 *>(to + lane * 64 + ((i ^ swz) << 4)) =
+                                        make_uint4(v[16 * h + 4 * i], v[16 * h + 4 * i + 1], v[16 * h + 4 * i + 2],
+                                                   v[16 * h + 4 * i + 3]);
+                                fence_async_shared();
+                                __syncwarp();
+                                const bool in = row0 < p.features && t.n0 + c + 16 * h < p.cols;
+                                if (elect_one()) {
+                                    if (!in)
+                                        ;  // (the empty group keeps the count of the buffers)
+                                    else if (add)
+                                        tma_add_3d(&p.c, smem_addr(to), t.n0 + c + 16 * h, row0, t.group);
+                                    else
+                                        tma_store_3d(&p.c, smem_addr(to), t.n0 + c + 16 * h, row0, t.group);
+                                    bulk_commit();
                                 }
-                            } else {
-                                uint32_t w[16];
+                            }
+                        } else {
+                            unsigned char *to = next_buffer();
+                            uint32_t w[16];
 #pragma unroll
-                                for (int i = 0; i < 32; i += 2)
-                                    swiglu::BF16::put2(w, i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                                store_row_chunk(static_cast<__nv_bfloat16 *>(p.out) + at, w, col, p.cols,
-                                                p.cols % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0);
+                            for (int i = 0; i < 32; i += 2)
+                                swiglu::BF16::put2(w, i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4 *>(to + lane * 64 + ((i ^ swz) << 4)) =
+                                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                            fence_async_shared();
+                            __syncwarp();
+                            if (elect_one()) {
+                                if (row0 < p.features && t.n0 + c < p.cols)
+                                    tma_store_3d(&p.c, smem_addr(to), t.n0 + c, row0, t.group);
+                                bulk_commit();
                             }
                         }
                     } else {
-                        // transposed through the warp's staging: a lane stores 32
-                        // features of one row
-                        __syncwarp();
+                        // transposed on the way to shared memory: row r of the buffer
+                        // is row c + r of the tile, its 16-byte pieces 8 features each
+                        unsigned char *to = next_buffer();
+                        const uint32_t at = smem_addr(to) + (lane & 7) * 64 +
+                                            (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) stg_warp[i * STG_ROW + lane] = __uint_as_float(v[i]);
-                        __syncwarp();
-                        const int col = t.m0 + 128 * (int)rank + 32 * quarter;
-                        if (c + lane < t.cnt && col < p.features) {
-                            uint32_t w[16];
+                        for (int j = 0; j < 4; ++j) {  // 8 rows each
+                            uint32_t w[4];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 a = lds128(stg_warp + lane * STG_ROW + 4 * i);
-                                swiglu::BF16::put2(w, 4 * i, a.x, a.y);
-                                swiglu::BF16::put2(w, 4 * i + 2, a.z, a.w);
+                            for (int m = 0; m < 4; ++m) {  // features 8 m ..
+                                const int r = 16 * (m >> 1) + 4 * j + 2 * (m & 1);
+                                uint32_t two[1];
+                                swiglu::BF16::put2(two, 0, __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
+                                w[m] = two[0];
                             }
-                            const int64_t row = (int64_t)t.r0 + t.n0 + c + lane;
-                            store_row_chunk(static_cast<__nv_bfloat16 *>(p.out) + row * p.features + col, w, col,
-                                            p.features,
-                                            p.features % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0);
+                            stmatrix_x4_trans(at + j * 8 * 64, w[0], w[1], w[2], w[3]);
+                        }
+                        const int col = t.m0 + 128 * (int)rank + 32 * quarter;
+                        const int row = t.r0 + t.n0 + c;
+                        const int live = t.cnt - c;
+                        if (live >= 32) {
+                            fence_async_shared();
+                            __syncwarp();
+                            if (elect_one()) {
+                                if (col < p.features) tma_store_2d(&p.c, smem_addr(to), col, row);
+                                bulk_commit();
+                            }
+                        } else {  // the rows after these are another group's
+                            if (elect_one()) bulk_commit();  // (an empty group: next_buffer counts them)
+                            __syncwarp();
+                            const int f = col + 8 * (lane & 3);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = 8 * i + (lane >> 2);
+                                const uint4 w = *reinterpret_cast<const uint4 *>(
+                                    to + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                                if (r < live && f < p.features)
+                                    store16(static_cast<__nv_bfloat16 *>(p.out) + (int64_t)(row + r) * p.features + f,
+                                            w.x, w.y, w.z, w.w);
+                            }
                         }
                     }
                 }
             } while (kb < kblocks);
         }
+        if (elect_one()) bulk_wait<0>();  // the stores, before their shared memory goes
     } else if (MODE == kWgrad && warp == 6) {
         // ---- zero the rows beyond the group in its last stage (both CTAs)
         int it = 0;
@@ -1058,6 +1114,16 @@ bool map3(EncodeTiled enc, CUtensorMap *map, const void *p, int64_t inner, int64
     return make_map(enc, map, p, 3, dims, strides, box);
 }
 
+// The result: boxes of 64 bytes by 32 rows with the 64-byte swizzle.
+bool out_map(EncodeTiled enc, CUtensorMap *map, void *p, int eb, int64_t inner, int64_t rows, int64_t outer) {
+    const cuuint64_t d[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
+    const cuuint64_t st[2] = {(cuuint64_t)(inner * eb), (cuuint64_t)(inner * rows * eb)};
+    const cuuint32_t box[3] = {(cuuint32_t)(64 / eb), 32, 1}, es[3] = {1, 1, 1};
+    return enc(map, eb == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+               outer > 0 ? 3 : 2, p, d, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The N side of the products over rows: boxes of 16, 32, 64 and 128 rows, as far
 // as a tile of `rows` rows (to 16) can need them; a CTA of a pair loads half of
 // its tile (to 32), which is no more.
@@ -1211,7 +1277,8 @@ swiglu_status_t swiglu_grouped_mm_fwd(const void *x, const void *w, const int32_
     const cudaError_t e = encoder(enc);
     if (e != cudaSuccess) return moe::cuda_fail(e);
     Params p{};
-    if (!map3(enc, &p.a, w, K, N, groups, 128, 1) || !row_maps(enc, p.b, x, K, rows))
+    if (!map3(enc, &p.a, w, K, N, groups, 128, 1) || !row_maps(enc, p.b, x, K, rows) ||
+        !out_map(enc, &p.c, y, 2, N, rows, 0))
         return moe::cuda_fail(cudaErrorInvalidValue);
     p.ends = ends;
     p.out = y;
@@ -1241,7 +1308,8 @@ swiglu_status_t swiglu_grouped_mm_dgrad(const void *dy, const void *w, const int
     if (e != cudaSuccess) return moe::cuda_fail(e);
     Params p{};
     // the contraction runs over W's rows: boxes of 64 columns by 64 of them
-    if (!map3(enc, &p.a, w, K, N, groups, BK, 1) || !row_maps(enc, p.b, dy, N, rows))
+    if (!map3(enc, &p.a, w, K, N, groups, BK, 1) || !row_maps(enc, p.b, dy, N, rows) ||
+        !out_map(enc, &p.c, dx, 2, K, rows, 0))
         return moe::cuda_fail(cudaErrorInvalidValue);
     p.ends = ends;
     p.out = dx;
@@ -1283,7 +1351,8 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     const cudaError_t e = encoder(enc);
     if (e != cudaSuccess) return moe::cuda_fail(e);
     Params p{};
-    if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK))
+    if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK) ||
+        !out_map(enc, &p.c, dw, eb, K, N, groups))
         return moe::cuda_fail(cudaErrorInvalidValue);
     p.ends = ends;
     p.out = dw;
