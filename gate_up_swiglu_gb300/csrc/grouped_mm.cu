@@ -22,16 +22,16 @@
 // rows and are loaded as they lie (MN-major descriptors): nothing is
 // transposed in memory.
 //
-// The roles of the 192 threads (224 for the weight gradient) of a CTA, the ring
-// of six 32 KiB stages, the two accumulators and the scheduling by cluster
-// launch control are those of fc1_swiglu.cu.  The number of tiles depends on
+// The ring of six 32 KiB stages, the two accumulators and the scheduling by
+// cluster launch control follow fc1_swiglu.cu; a warp of its own takes the tiles
+// and finds their groups.  The number of tiles depends on
 // the groups, which only the device knows: the grid holds as many clusters as
 // the sizes allow at most, and a pair that finds its tile beyond the last one
 // drops it.
 //
 // The weight gradient's contraction runs over a group's rows, so its last block
 // of 64 would take in rows of the next group.  Those loads are counted on a
-// barrier of their own, warp 6 of each CTA zeroes the rows beyond the group in
+// barrier of their own, warp 7 of each CTA zeroes the rows beyond the group in
 // shared memory (a product with 0 would not do: a neighbour's row may hold
 // NaN), and only then the stage is handed to the tensor cores.
 #include <climits>
@@ -63,8 +63,7 @@ constexpr int kGroupN = 16;          // N tiles per block of the tile order
 // are added with rounded fp32 additions
 constexpr int kSegmentRows = 4096;
 
-constexpr int kTileSlots = 4;
-constexpr int kAskAhead = 16;
+constexpr int kTileSlots = 3;        // tiles taken ahead, at most
 // byte offsets in the region after the ring
 constexpr int OFF_FULL = 0;
 constexpr int OFF_EMPTY = OFF_FULL + 8 * STAGES;
@@ -76,8 +75,8 @@ constexpr int OFF_TILE_FULL = OFF_MMA_DONE + 8;
 constexpr int OFF_TILE_EMPTY = OFF_TILE_FULL + 8 * kTileSlots;
 constexpr int OFF_CLC_BAR = OFF_TILE_EMPTY + 8 * kTileSlots;
 constexpr int OFF_CLC_RESP = (OFF_CLC_BAR + 8 + 15) / 16 * 16;
-constexpr int OFF_TILE_ID = OFF_CLC_RESP + 16;
-constexpr int OFF_TMEM = OFF_TILE_ID + 4 * kTileSlots;
+constexpr int OFF_TILE = (OFF_CLC_RESP + 16 + 31) / 32 * 32;  // tile[kTileSlots], 32 bytes each
+constexpr int OFF_TMEM = OFF_TILE + 32 * kTileSlots;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
 constexpr int STATE_BYTES = 512;
 static_assert(OFF_ABORT + 4 <= STATE_BYTES, "barriers and state fit their region");
@@ -138,6 +137,30 @@ struct Tile {
     int group, m0, n0, cnt;  // first feature, first row (kWgrad: column), rows (kWgrad: columns)
     int r0, rows;            // the group's rows
 };
+
+// Write a tile (group -1: none left) into the slot at `slot` of both CTAs and
+// release it with an arrive on each CTA's barrier; read one.
+__device__ __forceinline__ void publish(uint32_t slot, uint32_t bar, const Tile &t) {
+#pragma unroll
+    for (uint32_t r = 0; r < 2; ++r) {
+        const uint32_t to = map_to_rank(slot, r);
+        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(t.group), "r"(t.m0), "r"(t.n0),
+                     "r"(t.cnt)
+                     : "memory");
+        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to + 16), "r"(t.r0), "r"(t.rows) : "memory");
+        mbar_arrive_cluster(map_to_rank(bar, r));
+    }
+}
+
+__device__ __forceinline__ Tile read_tile(uint32_t slot) {
+    Tile t;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(t.group), "=r"(t.m0), "=r"(t.n0), "=r"(t.cnt)
+                 : "r"(slot)
+                 : "memory");
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(t.r0), "=r"(t.rows) : "r"(slot + 16) : "memory");
+    return t;
+}
 
 // Fill starts and base (one warp) for tiles of TF features by at most TN rows
 // (kWgrad: columns).  The last "group" is that of the rows that belong to none.
@@ -282,8 +305,13 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int m, int 
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// Warps: 0 loads, 1 MMA, 2 - 5 epilogue, 6 scheduler, 7 (kWgrad) zeroes rows.
+constexpr int kScheduler = 6, kZeroWarp = 7;
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224 : 192, 1)
+constexpr int kPairThreads = 32 * (MODE == kWgrad ? 8 : 7);
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 1)
     grouped_mm_kernel(const __grid_constant__ Params p) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -297,8 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
     const uint32_t mma_done = st0 + OFF_MMA_DONE;
     const uint32_t tile_full0 = st0 + OFF_TILE_FULL, tile_empty0 = st0 + OFF_TILE_EMPTY;
     const uint32_t clc_bar = st0 + OFF_CLC_BAR, clc_resp = st0 + OFF_CLC_RESP;
-    const uint32_t tile_ids_addr = st0 + OFF_TILE_ID;
-    volatile int *tile_ids = reinterpret_cast<volatile int *>(state + OFF_TILE_ID);
+    const uint32_t tile0 = st0 + OFF_TILE;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(state + OFF_ABORT);
     int *starts = reinterpret_cast<int *>(state + STATE_BYTES);
@@ -306,9 +333,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
 
     constexpr bool kAMn = MODE == kDgrad || MODE == kWgrad;
     constexpr bool kBMn = MODE == kWgrad;
-    // readers of a tile id: the peer's producer, the MMA thread, the epilogue
-    // warps of both CTAs and, for the weight gradient, the warps that zero rows
-    constexpr int kReaders = 1 + 1 + 2 * 4 + (MODE == kWgrad ? 2 : 0);
+    // readers of a tile: the MMA thread and, of both CTAs, the producer, the
+    // epilogue warps and, for the weight gradient, the warp that zeroes rows
+    constexpr int kReaders = 1 + 2 * (1 + 4 + (MODE == kWgrad ? 1 : 0));
 
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
@@ -318,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             // kWgrad: an arrival for each CTA's half (both by the leader's producer,
-            // or warp 6 of each once the rows beyond the group are zero)
+            // or warp 7 of each once the rows beyond the group are zero)
             mbar_init(full0 + 8 * s, MODE == kWgrad ? 2 : 1);
             mbar_init(empty0 + 8 * s, 1);
             mbar_init(tail0 + 8 * s, 1);
@@ -365,58 +392,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
     // contraction blocks per accumulation (kWgrad with fp32 results: a segment)
     const int seg_blocks = MODE == kWgrad && p.f32_out ? kSegmentRows / BK : INT_MAX;
 
-    if (warp == 0 && elect_one()) {
-        // ---- producer (both CTAs); the leader's also schedules.  (With the
-        // thread picked by `lane == 0` each load cost ~400 cycles to issue: 8192 x
-        // 4096 x 8192 1390 TFLOP/s with three loads a stage, 740 with four,
-        // against 1875 and 814.)
-        int it = 0, asks = 0;
-        int tile = (int)(blockIdx.x >> 1);
-        bool asked = false;
-        const auto ask = [&]() {
-            mbar_arrive_expect_tx(clc_bar, 16);
-            clc_try_cancel(clc_resp, clc_bar);
-            asked = true;
-        };
-        // the next tile: -1 when no pending cluster was left to take
-        const auto answer = [&]() {
-            asked = false;
-            // waited for even after an abort, so that it never lands in shared
-            // memory the CTA has left
-            if (!mbar_wait<true>(clc_bar, asks++ & 1)) return -1;
-            const int x = clc_cancelled_cta(clc_resp);
-            if (x < 0) return -1;
-            if ((x & 1) != 0 || x >= (int)gridDim.x) {  // not a cluster's first CTA of this grid
-                *abort_flag = 1;
-                atomicExch(&g_timeout, 1);
-                return -1;
-            }
-            return x >> 1;
-        };
-        for (int k = 0;; ++k) {
-            const int slot = k % kTileSlots;
-            if (leader) {
-                while (tile >= tiles) {  // beyond the last tile: take another cluster
-                    ask();
-                    tile = answer();
-                }
-                if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) {
+    // tile k of this pair, for a single thread; group -1 when none is left
+    const auto next_tile = [&](int k) {
+        const int slot = k % kTileSlots;
+        Tile t;
+        t.group = -1;
+        if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1)) t = read_tile(tile0 + 32 * slot);
+        mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+        return t;
+    };
+    // the same for a whole warp
+    const auto next_tile_warp = [&](int k) {
+        const int slot = k % kTileSlots;
+        const bool ok =
+            __all_sync(0xffffffffu, mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1));
+        Tile t = read_tile(tile0 + 32 * slot);
+        if (!ok) t.group = -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+        return t;
+    };
+
+    if (warp == kScheduler) {
+        // ---- scheduler (the leader's): takes tiles and publishes them to both
+        // CTAs, up to kTileSlots ahead of the slowest reader, so that neither the
+        // cancellation's latency nor finding a tile's group delays the loads
+        if (leader && elect_one()) {
+            int tile = (int)(blockIdx.x >> 1), asks = 0;
+            // take another cluster's tile; -1 when no pending one was left
+            const auto take = [&]() {
+                mbar_arrive_expect_tx(clc_bar, 16);
+                clc_try_cancel(clc_resp, clc_bar);
+                if (!mbar_wait<true>(clc_bar, asks++ & 1)) return -1;
+                const int x = clc_cancelled_cta(clc_resp);
+                if (x < 0) return -1;
+                if ((x & 1) != 0 || x >= (int)gridDim.x) {  // not a cluster's first CTA of this grid
                     *abort_flag = 1;
-                    tile = -1;
+                    atomicExch(&g_timeout, 1);
+                    return -1;
                 }
-                publish_tile(tile_ids_addr, tile_full0, slot, tile);
-            } else {
-                tile = mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1) ? tile_ids[slot] : -1;
-                mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+                return x >> 1;
+            };
+            for (int k = 0;; ++k) {
+                const int slot = k % kTileSlots;
+                while (tile >= tiles) tile = take();  // beyond the last tile
+                Tile t;
+                t.group = -1;
+                if (tile >= 0) t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
+                if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) *abort_flag = 1;
+                if (*abort_flag) t.group = -1;
+                publish(tile0 + 32 * slot, tile_full0 + 8 * slot, t);
+                if (t.group < 0) break;
+                tile = take();
             }
-            if (tile < 0) break;
-            const Tile t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
+        }
+    } else if (warp == 0 && elect_one()) {
+        // ---- producer (both CTAs).  (With the thread picked by `lane == 0` each load
+        // cost ~400 cycles to issue: 8192 x 4096 x 8192 ran at 1390 TFLOP/s with
+        // three loads a stage and 740 with four, against 1875 and 814.)
+        int it = 0;
+        for (int k = 0;; ++k) {
+            const Tile t = next_tile(k);
+            if (t.group < 0) break;
             const int kblocks = blocks_of(t);
             const int half = width_of(t) / 2;  // this CTA's rows of the N side
             const uint32_t bytes = (uint32_t)(A_BYTES + half * BK * 2);
-            const int ask_at = kblocks > kAskAhead ? kblocks - kAskAhead : 0;
             for (int kb = 0; kb < kblocks && !*abort_flag; ++kb, ++it) {
-                if (leader && kb == ask_at) ask();
                 const int s = it % STAGES;
                 if (!mbar_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1)) {
                     *abort_flag = 1;
@@ -425,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
                 const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
                 uint32_t bar = map_to_rank(full0 + 8 * s, 0);
                 if (MODE == kWgrad && (kb + 1) * BK > t.rows) {
-                    // rows beyond the group: warp 6 of each CTA hands its half on
+                    // rows beyond the group: warp 7 of each CTA hands its half on
                     bar = map_to_rank(tail0 + 8 * s, rank);
                     mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
                 } else if (leader) {
@@ -469,11 +510,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
                     }
                 }
             }
-            if (leader) {
-                if (!asked && !*abort_flag) ask();
-                tile = asked ? answer() : -1;
-                if (*abort_flag) tile = -1;
-            }
         }
         // the leader's full barriers count both CTAs' bytes: once their last
         // phases complete, every load of the pair has landed
@@ -485,11 +521,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
         int it = 0, lt = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            const int slot = k % kTileSlots;
-            const int tile = mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1) ? tile_ids[slot] : -1;
-            mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
-            if (tile < 0 || *abort_flag) break;
-            const Tile t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
+            const Tile t = next_tile(k);
+            if (t.group < 0 || *abort_flag) break;
             const int kblocks = blocks_of(t);
             const uint32_t idesc = instr_desc(kAMn, kBMn, 256, width_of(t));
             int kb = 0;
@@ -555,17 +588,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
         // the warp leaves the loop as one: the tile id, the abort flag and the
         // waits' outcome are warp-uniform
         for (int k = 0; ok; ++k) {
-            const int slot = k % kTileSlots;
-            int tile = -1;
-            if (lane == 0) {
-                if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1)) tile = tile_ids[slot];
-                mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
-            }
-            tile = __shfl_sync(0xffffffffu, tile, 0);
+            const Tile t = next_tile_warp(k);
             // the barriers below need both warps of a pair, so the two leave
             // together, whichever of them gave up on its wait
-            if (MODE == kFc1 ? any_of_pair(bar_id, tile < 0) : tile < 0) break;
-            const Tile t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
+            if (MODE == kFc1 ? any_of_pair(bar_id, t.group < 0) : t.group < 0) break;
             const int kblocks = blocks_of(t);
             const int width = width_of(t);
             int kb = 0;
@@ -770,20 +796,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kWgrad ? 224
             } while (kb < kblocks);
         }
         if (elect_one()) bulk_wait<0>();  // the stores, before their shared memory goes
-    } else if (MODE == kWgrad && warp == 6) {
+    } else if (MODE == kWgrad && warp == kZeroWarp) {
         // ---- zero the rows beyond the group in its last stage (both CTAs)
         int it = 0;
         uint32_t uses = 0;  // phase of each stage's tail barrier
         for (int k = 0;; ++k) {
-            const int slot = k % kTileSlots;
-            int tile = -1;
-            if (lane == 0) {
-                if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1)) tile = tile_ids[slot];
-                mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
-            }
-            tile = __shfl_sync(0xffffffffu, tile, 0);
-            if (tile < 0) break;
-            const Tile t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
+            const Tile t = next_tile_warp(k);
+            if (t.group < 0) break;
             it += blocks_of(t);
             const int live = t.rows % BK;
             if (live == 0) continue;
@@ -1146,7 +1165,7 @@ swiglu_status_t launch_kernel(const Params &p, int64_t clusters, swiglu_stream_t
         if (e != cudaSuccess) return moe::cuda_fail(e);
         if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true);
     }
-    e = moe::launch(grouped_mm_kernel<MODE>, dim3((unsigned)(2 * clusters)), MODE == kWgrad ? 224 : 192, SMEM_BYTES,
+    e = moe::launch(grouped_mm_kernel<MODE>, dim3((unsigned)(2 * clusters)), kPairThreads<MODE>, SMEM_BYTES,
                     stream, 0, p);
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
