@@ -116,7 +116,7 @@ struct Params {
     uint8_t *scales;
     int rows, groups;
     int features;    // kFc1: n; kMm: N; kDgrad: K; kWgrad: N
-    int cols;        // kWgrad: K
+    int cols;        // kWgrad: K (split kernel: features K and cols N)
     int depth;       // contraction length (kWgrad: unused)
     int f32_out, accumulate;  // kWgrad
 };
@@ -610,20 +610,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                 ++lt;
                 tc_fence_after();
                 const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
+                // (reading the next 32 columns ahead of storing these was no faster:
+                // 4.7 us per 256 x 256 tile of one contraction block against 4.3)
 #pragma unroll 1
                 for (int c = 0; c < width; c += 32) {
                     uint32_t v[32];
                     if constexpr (MODE == kMm || MODE == kDgrad) {
-                        uint32_t lo[16], hi[16];  // lanes 0 - 15 and 16 - 31 of the quarter
-                        tmem_load_16x32(tbase + c, lo);
-                        tmem_load_16x32(tbase + (16u << 16) + c, hi);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = lo[i], v[16 + i] = hi[i];
+                        tmem_load_16x32(tbase + c, v);  // lanes 0 - 15 and 16 - 31 of the quarter
+                        tmem_load_16x32(tbase + (16u << 16) + c, v + 16);
                     } else {
                         tmem_load32(tbase + c, v);
-                        tmem_wait_ld();
                     }
+                    tmem_wait_ld();
                     if (c + 32 >= width) {
                         tc_fence_before();
                         __syncwarp();
@@ -867,8 +865,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
     return v;
 }
 
@@ -889,12 +886,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
     constexpr int kStages = kSplitStages<NT>;
     constexpr int kStage = kSplitStageBytes<NT>;
     const uint32_t full0 = st0, empty0 = st0 + 8 * kStages, acc_full = st0 + 16 * kStages;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + 16 * kStages + 8);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(state + 16 * kStages + 12);
-    static_assert(16 * kStages + 16 <= STATE_BYTES, "barriers and state fit their region");
+    const uint32_t landed = acc_full + 8, zeroed = acc_full + 16;  // of a group's last block (kWgrad)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + 16 * kStages + 24);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(state + 16 * kStages + 28);
+    static_assert(16 * kStages + 32 <= STATE_BYTES, "barriers and state fit their region");
     int *starts = reinterpret_cast<int *>(state + STATE_BYTES);
     int *base = starts + kMaxGroups + 2;
-    constexpr bool kAMn = MODE == kDgrad;
+    constexpr bool kAMn = MODE == kDgrad || MODE == kWgrad, kBMn = MODE == kWgrad;
+    static_assert(MODE != kWgrad || NT == 128, "the weight gradient's N side comes in boxes of 64 columns");
 
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -904,6 +903,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
             mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(acc_full, 1);
+        mbar_init(landed, 1);
+        mbar_init(zeroed, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
@@ -930,21 +931,26 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
     if (live) {
         t = tile_at<MODE, kSplitF<MODE>, NT, 16>(p, groups, tile);
         if (t.group != p.groups) {
-            const int kblocks = (p.depth + BK - 1) / BK;
+            const int kblocks = ((MODE == kWgrad ? t.rows : p.depth) + BK - 1) / BK;
             kb0 = (int)((int64_t)kblocks * rank / size);
             kb1 = (int)((int64_t)kblocks * (rank + 1) / size);
         }
     }
     const int width = (t.cnt + 15) / 16 * 16;
+    // kWgrad: the rows of the group's last block, where it is this CTA's and not full
+    const int last_rows = MODE == kWgrad && kb1 > kb0 && kb1 * BK > t.rows ? t.rows % BK : 0;
     if (warp == 0 && elect_one()) {
-        const uint32_t bytes = (uint32_t)(A_BYTES + width * BK * 2);
+        const int box_cols = (width + 63) / 64;  // kWgrad
+        const uint32_t bytes =
+            (uint32_t)(A_BYTES + (MODE == kWgrad ? box_cols * (A_BYTES / 2) : width * BK * 2));
         for (int kb = kb0, it = 0; kb < kb1 && !*abort_flag; ++kb, ++it) {
             const int s = it % kStages;
             if (!mbar_wait(empty0 + 8 * s, ((it / kStages) & 1) ^ 1)) {
                 *abort_flag = 1;
                 break;
             }
-            const uint32_t sa = ring + s * kStage, bar = full0 + 8 * s;
+            const uint32_t sa = ring + s * kStage;
+            const uint32_t bar = last_rows != 0 && kb == kb1 - 1 ? landed : full0 + 8 * s;
             mbar_arrive_expect_tx(bar, bytes);
             if (MODE == kFc1) {
 #pragma unroll
@@ -952,10 +958,17 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
                     tma_load_3d(sa + i * (A_BYTES / 2), &p.a, bar, kb * BK, t.m0 + 32 * i, 2 * t.group);
             } else if (MODE == kMm) {
                 tma_load_3d(sa, &p.a, bar, kb * BK, t.m0, t.group);
-            } else {
+            } else if (MODE == kDgrad) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     tma_load_3d(sa + i * (A_BYTES / 2), &p.a, bar, t.m0 + 64 * i, kb * BK, t.group);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    tma_load_2d(sa + i * (A_BYTES / 2), &p.a, bar, t.m0 + 64 * i, t.r0 + kb * BK);
+                for (int i = 0; i < box_cols; ++i)
+                    tma_load_2d(sa + A_BYTES + i * (A_BYTES / 2), &p.b[0], bar, t.n0 + 64 * i, t.r0 + kb * BK);
+                continue;
             }
             int row = t.r0 + t.n0;
             uint32_t dst = sa + A_BYTES;
@@ -969,10 +982,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
             }
         }
     } else if (warp == 1 && kb1 > kb0 && elect_one()) {
-        const uint32_t idesc = instr_desc(kAMn, false, 128, width);
+        const uint32_t idesc = instr_desc(kAMn, kBMn, 128, width);
         for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
             const int s = it % kStages;
-            if (!mbar_wait(full0 + 8 * s, (it / kStages) & 1)) {
+            if (!(last_rows != 0 && kb == kb1 - 1 ? mbar_wait(zeroed, 0)
+                                                  : mbar_wait(full0 + 8 * s, (it / kStages) & 1))) {
                 *abort_flag = 1;
                 break;
             }
@@ -982,7 +996,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
             for (int kk = 0; kk < BK / UMMA_K; ++kk) {
                 const uint64_t a = kAMn ? smem_desc_128b(sa + kk * UMMA_K * 128, A_BYTES / 2)
                                         : smem_desc_128b(sa + kk * UMMA_K * 2);
-                mma_bf16(tmem, a, smem_desc_128b(sb + kk * UMMA_K * 2), idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
+                const uint64_t b = kBMn ? smem_desc_128b(sb + kk * UMMA_K * 128, A_BYTES / 2)
+                                        : smem_desc_128b(sb + kk * UMMA_K * 2);
+                mma_bf16(tmem, a, b, idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
             }
             mma_commit(empty0 + 8 * s);
         }
@@ -992,6 +1008,20 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
         // of the ring has been consumed by then
         const int quarter = warp & 3;
         float *part = reinterpret_cast<float *>(smem);
+        if (MODE == kWgrad && last_rows != 0 && warp == 2) {
+            // zero the next group's rows in the last block, as in the pair kernel
+            if (!__all_sync(0xffffffffu, mbar_wait(landed, 0)) && lane == 0) *abort_flag = 1;
+            unsigned char *stage = smem + (kb1 - 1 - kb0) % kStages * kStage;
+            for (int i = lane; i < (BK - last_rows) * 8; i += 32) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    *reinterpret_cast<uint4 *>(stage + b * (A_BYTES / 2) + last_rows * 128 + i * 16) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(zeroed);
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(acc_full, 0)) && lane == 0) *abort_flag = 1;
         tc_fence_after();
 #pragma unroll 1
@@ -1009,86 +1039,131 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
     if (size > 1) cluster_sync();
     if (live) {
         // rows rank, rank + S, ... of the tile: 16 (kFc1) or 32 threads a row, four
-        // features each, summed over the slices in rank order
+        // features each, summed over the slices in rank order; kAtOnce rows of a
+        // thread in flight, as a load from another SM takes long
         constexpr int kRowThreads = kSplitF<MODE> / 4;
-        const int slices = t.group == p.groups ? 0 : (int)size;
-        const uint32_t part0 = ring;
-        const int f = (int)threadIdx.x % kRowThreads;  // (kSplitThreads is a multiple of kRowThreads)
+        constexpr int kPass = kSplitThreads / kRowThreads;  // rows of the CTA per pass
+        constexpr int kAtOnce = 4;
+        static_assert(kSplitThreads % kRowThreads == 0, "whole rows of threads");
+        uint32_t have = 0;  // slices with a block (a short group of kWgrad leaves some without)
+        if (t.group != p.groups) {
+            const int blocks = ((MODE == kWgrad ? t.rows : p.depth) + BK - 1) / BK;
+            for (uint32_t s = 0; s < size; ++s)
+                if ((int64_t)blocks * s / size < (int64_t)blocks * (s + 1) / size) have |= 1u << s;
+        }
+        const int f = (int)threadIdx.x % kRowThreads;
         // kFc1: 32 gates, 32 ups, 32 gates, 32 ups
         const int lane0 = MODE == kFc1 ? f / 8 * 64 + f % 8 * 4 : f * 4;
         const int col = t.m0 + 4 * f;
-        for (int r0 = (int)rank; r0 < t.cnt; r0 += (int)size * (kSplitThreads / kRowThreads)) {
-            // the same trip count for a whole warp: the block maximum is shuffled
-            const int r = r0 + (int)(threadIdx.x / kRowThreads) * (int)size;
-            const bool in = r < t.cnt && col < p.features;
-            float g[4] = {}, u[4] = {};
-            if (in) {
-                for (int s = 0; s < slices; ++s) {
-                    const uint32_t at = map_to_rank(part0 + (uint32_t)(r * kPartialRow + lane0) * 4, (uint32_t)s);
-                    const float4 a = ld_cluster(at);
-                    g[0] = __fadd_rn(g[0], a.x), g[1] = __fadd_rn(g[1], a.y);
-                    g[2] = __fadd_rn(g[2], a.z), g[3] = __fadd_rn(g[3], a.w);
-                    if (MODE == kFc1) {
-                        const float4 b = ld_cluster(at + 32 * 4);
-                        u[0] = __fadd_rn(u[0], b.x), u[1] = __fadd_rn(u[1], b.y);
-                        u[2] = __fadd_rn(u[2], b.z), u[3] = __fadd_rn(u[3], b.w);
-                    }
-                }
-            }
-            const int64_t row = (int64_t)t.r0 + t.n0 + r;
-            const auto pack = [](const float (&v)[4], uint32_t (&w)[2]) {
-                swiglu::BF16::put2(w, 0, v[0], v[1]);
-                swiglu::BF16::put2(w, 2, v[2], v[3]);
-            };
-            using St8 = swiglu::St<8, swiglu::kStStream>;
-            if constexpr (MODE == kFc1) {
-                const int n = p.features;
-                if (p.q != nullptr) {
-                    float mg = ckpt8::finite_amax<4>(g), mu = ckpt8::finite_amax<4>(u);
+        const int step = kPass * (int)size;
+        // (the trip counts are the same for a whole warp: the block maximum is shuffled)
+        for (int r0 = (int)rank; r0 < t.cnt; r0 += kAtOnce * step) {
+            const int first = r0 + (int)(threadIdx.x / kRowThreads) * (int)size;
+            float gs[kAtOnce][4] = {}, us[MODE == kFc1 ? kAtOnce : 1][4] = {};
+            if (col < p.features) {
+                for (uint32_t s = 0; s < size; ++s) {
+                    if (!(have >> s & 1)) continue;
+                    const uint32_t from = map_to_rank(ring + (uint32_t)(first * kPartialRow + lane0) * 4, s);
+                    float4 a[kAtOnce], b[kAtOnce];
 #pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) {  // eight threads hold a block
-                        mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-                        mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        if (first + i * step < t.cnt) {
+                            a[i] = ld_cluster(from + (uint32_t)(i * step * kPartialRow) * 4);
+                            if (MODE == kFc1) b[i] = ld_cluster(from + (uint32_t)(i * step * kPartialRow + 32) * 4);
+                        }
                     }
-                    if (in) {
-                        const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
-                        uint32_t qg, qu;
-                        ckpt8::encode<4>(g, ckpt8::encode_factor(cg), &qg);
-                        ckpt8::encode<4>(u, ckpt8::encode_factor(cu), &qu);
-                        uint8_t *qr = p.q + row * 2 * n + col;
-                        swiglu::St<4, swiglu::kStStream>::run(qr, &qg);
-                        swiglu::St<4, swiglu::kStStream>::run(qr + n, &qu);
-                        if (f % 8 == 0) {
-                            const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
-                            uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
-                            sr[0] = (uint8_t)cg;
-                            sr[nb] = (uint8_t)cu;
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        if (first + i * step < t.cnt) {
+                            gs[i][0] = __fadd_rn(gs[i][0], a[i].x), gs[i][1] = __fadd_rn(gs[i][1], a[i].y);
+                            gs[i][2] = __fadd_rn(gs[i][2], a[i].z), gs[i][3] = __fadd_rn(gs[i][3], a[i].w);
+                            if constexpr (MODE == kFc1) {
+                                us[i][0] = __fadd_rn(us[i][0], b[i].x), us[i][1] = __fadd_rn(us[i][1], b[i].y);
+                                us[i][2] = __fadd_rn(us[i][2], b[i].z), us[i][3] = __fadd_rn(us[i][3], b[i].w);
+                            }
                         }
                     }
                 }
-                if (in) {
-                    uint32_t w[2];
-                    if (p.fc1 != nullptr) {
-                        __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
-                        pack(g, w);
-                        St8::run(fr, w);
-                        pack(u, w);
-                        St8::run(fr + n, w);
-                    }
-                    const float wr = p.probs != nullptr && t.group != p.groups ? p.probs[row] : 1.0f;
-                    float y[4];
+            }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const swiglu::Act act = swiglu::activation<swiglu::BF16, false, true>(g[i]);
-                        y[i] = __fmul_rn(__fmul_rn(__fmul_rn(act.silu, u[i]), wr), act.scale);
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (r0 + i * step >= t.cnt) break;
+                const int r = first + i * step;
+                const bool in = r < t.cnt && col < p.features;
+                float(&g)[4] = gs[i];
+                float(&u)[4] = us[MODE == kFc1 ? i : 0];
+                const int64_t row = (int64_t)t.r0 + t.n0 + r;
+                const auto pack = [](const float (&v)[4], uint32_t (&w)[2]) {
+                    swiglu::BF16::put2(w, 0, v[0], v[1]);
+                    swiglu::BF16::put2(w, 2, v[2], v[3]);
+                };
+                using St8 = swiglu::St<8, swiglu::kStStream>;
+                if constexpr (MODE == kFc1) {
+                    const int n = p.features;
+                    if (p.q != nullptr) {
+                        float mg = ckpt8::finite_amax<4>(g), mu = ckpt8::finite_amax<4>(u);
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) {  // eight threads hold a block
+                            mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+                            mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+                        }
+                        if (in) {
+                            const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
+                            uint32_t qg, qu;
+                            ckpt8::encode<4>(g, ckpt8::encode_factor(cg), &qg);
+                            ckpt8::encode<4>(u, ckpt8::encode_factor(cu), &qu);
+                            uint8_t *qr = p.q + row * 2 * n + col;
+                            swiglu::St<4, swiglu::kStStream>::run(qr, &qg);
+                            swiglu::St<4, swiglu::kStStream>::run(qr + n, &qu);
+                            if (f % 8 == 0) {
+                                const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
+                                uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
+                                sr[0] = (uint8_t)cg;
+                                sr[nb] = (uint8_t)cu;
+                            }
+                        }
                     }
-                    pack(y, w);
-                    St8::run(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, w);
+                    if (in) {
+                        uint32_t w[2];
+                        if (p.fc1 != nullptr) {
+                            __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
+                            pack(g, w);
+                            St8::run(fr, w);
+                            pack(u, w);
+                            St8::run(fr + n, w);
+                        }
+                        const float wr = p.probs != nullptr && t.group != p.groups ? p.probs[row] : 1.0f;
+                        float y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const swiglu::Act act = swiglu::activation<swiglu::BF16, false, true>(g[i]);
+                            y[i] = __fmul_rn(__fmul_rn(__fmul_rn(act.silu, u[i]), wr), act.scale);
+                        }
+                        pack(y, w);
+                        St8::run(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, w);
+                    }
+                } else if (MODE == kWgrad && in) {
+                    // the M side are dW's columns, the N side its rows
+                    const int64_t at = ((int64_t)t.group * p.cols + t.n0 + r) * p.features + col;
+                    if (p.f32_out) {
+                        float *o = static_cast<float *>(p.out) + at;
+                        if (p.accumulate) {
+                            const float4 old = *reinterpret_cast<const float4 *>(o);
+                            g[0] = __fadd_rn(old.x, g[0]), g[1] = __fadd_rn(old.y, g[1]);
+                            g[2] = __fadd_rn(old.z, g[2]), g[3] = __fadd_rn(old.w, g[3]);
+                        }
+                        store16(o, __float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
+                                __float_as_uint(g[3]));
+                    } else {
+                        uint32_t w[2];
+                        pack(g, w);
+                        St8::run(static_cast<__nv_bfloat16 *>(p.out) + at, w);
+                    }
+                } else if (in) {
+                    uint32_t w[2];
+                    pack(g, w);
+                    St8::run(static_cast<__nv_bfloat16 *>(p.out) + row * p.features + col, w);
                 }
-            } else if (in) {
-                uint32_t w[2];
-                pack(g, w);
-                St8::run(static_cast<__nv_bfloat16 *>(p.out) + row * p.features + col, w);
             }
         }
     }
@@ -1196,23 +1271,59 @@ swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_st
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
 
-// Launch a product over rows.  Pairs of CTAs while there are tiles for at least
-// kPairsWanted of them; below that the split kernel, with as many CTAs per tile
-// as keep the grid within two per SM (and two blocks of depth per CTA at least).
-constexpr int64_t kPairsWanted = 76;
-constexpr int64_t kSplitCtas = 304;
+// Pairs or split?  Both kernels are bound by the operand bytes that an SM takes
+// in (about 100 GB/s were seen), so the rule compares, per block of depth, the
+// bytes of a CTA's stage times the rounds that its grid takes on the 152 SMs.
+// It counts the tiles of groups of equal size, which is all the host knows.  The
+// split kernel's least cost over S adds the other constants: times as bytes at
+// that rate (100 KiB: 1 us).
+struct Plan {
+    int size;  // CTAs per tile of the split kernel; 0: pairs
+};
+constexpr int kSms = 152;
+constexpr int64_t kJoin = 100 * 1024;
+constexpr int64_t kPairs = 500 * 1024;      // the pairs' way in and out
+constexpr int64_t kPairTile = 430 * 1024;   // a pair's tile at least: its epilogue
+constexpr int64_t kSplitTile = 300 * 1024;  // a CTA's way in and out, once per tile
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// `rows_per`: N extent of a group's tiles (rows, or columns of dW); `same`: groups
+// with that extent; features: the M extent; pair_f / split_f: features of a tile.
+Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int split_f, int nt, int64_t kblocks) {
+    const int64_t pair_n = rows_per < TILE_N ? ceil_div(rows_per, 32) * 32 : TILE_N;
+    const int64_t pair_tiles = same * ceil_div(rows_per, TILE_N) * ceil_div(features, pair_f);
+    const int64_t pair_depth = kblocks * (A_BYTES + pair_n * BK);
+    const int64_t pair_cost =
+        ceil_div(pair_tiles, kSms / 2) * (pair_depth > kPairTile ? pair_depth : kPairTile) + kPairs;
+    const int64_t split_n = rows_per < nt ? ceil_div(rows_per, 16) * 16 : nt;
+    const int64_t split_tiles = same * ceil_div(rows_per, nt) * ceil_div(features, split_f);
+    Plan best = {0};
+    int64_t least = pair_cost;
+    for (int size = 1; size <= 8 && (size == 1 || 2 * size <= kblocks); size *= 2) {
+        const int64_t cost = ceil_div(split_tiles * size, kSms) *
+                                 (ceil_div(kblocks, size) * (A_BYTES + split_n * BK * 2) + kSplitTile) +
+                             (size > 1 ? kJoin : 0);
+        if (cost < least) {
+            least = cost;
+            best.size = size;
+        }
+    }
+    return best;
+}
+
+// Launch a product over rows.
 template <int MODE>
 swiglu_status_t launch_rows(const Params &p, swiglu_stream_t stream) {
     const int64_t pairs = most_tiles(p.rows, p.groups, p.features, kTileF<MODE>, TILE_N);
     if (pairs > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
-    if (pairs >= kPairsWanted) return launch_kernel<MODE>(p, pairs, stream);
     const bool few = p.rows <= 32;
+    const int64_t same = p.rows < p.groups ? p.rows : p.groups;
+    const Plan pl = plan(same, ceil_div(p.rows, same), p.features, kTileF<MODE>, kSplitF<MODE>, few ? 32 : 128,
+                         ceil_div(p.depth, BK));
     const int64_t tiles = most_tiles(p.rows, p.groups, p.features, kSplitF<MODE>, few ? 32 : 128);
-    const int kblocks = (p.depth + BK - 1) / BK;
-    int size = 1;
-    while (size < 8 && tiles * size * 2 <= kSplitCtas && size * 4 <= kblocks) size *= 2;
-    return few ? launch_split<MODE, 32>(p, tiles, size, stream) : launch_split<MODE, 128>(p, tiles, size, stream);
+    if (pl.size == 0 || tiles > INT32_MAX / 16) return launch_kernel<MODE>(p, pairs, stream);
+    return few ? launch_split<MODE, 32>(p, tiles, pl.size, stream) : launch_split<MODE, 128>(p, tiles, pl.size, stream);
 }
 
 // The checks that the products share.
@@ -1363,25 +1474,36 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     if (!span_of(dy, rows, N, N, 2, sdy) || !span_of(x, rows, K, K, 2, sx) || !span_of(ends, groups, 1, 1, 4, se))
         return SWIGLU_ERR_SHAPE;
     if (moe::any_alias({sdw}, {sdy, sx, se})) return SWIGLU_ERR_ALIAS;
-    const int64_t clusters = groups * ((N + 255) / 256) * ((K + TILE_N - 1) / TILE_N);
-    if (clusters > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
+    const int64_t pairs = groups * ceil_div(N, 256) * ceil_div(K, TILE_N);
+    if (pairs > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
 
     EncodeTiled enc;
     const cudaError_t e = encoder(enc);
     if (e != cudaSuccess) return moe::cuda_fail(e);
     Params p{};
-    if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK) ||
-        !out_map(enc, &p.c, dw, eb, K, N, groups))
-        return moe::cuda_fail(cudaErrorInvalidValue);
     p.ends = ends;
     p.out = dw;
     p.rows = (int)rows;
     p.groups = (int)groups;
-    p.features = (int)N;
-    p.cols = (int)K;
     p.f32_out = dw_dtype == SWIGLU_F32;
     p.accumulate = accumulate != 0;
-    return launch_kernel<kWgrad>(p, clusters, stream);
+    // Pairs: M is dW's rows, N its columns.  Split: the other way round, so that the
+    // lanes run along dW's rows; an fp32 sum's slices stay within a segment.
+    Plan pl = plan(groups, N, K, 256, kSplitF<kWgrad>, 128, ceil_div(ceil_div(rows, groups), BK));
+    if (p.f32_out && rows / (pl.size > 0 ? pl.size : 1) > kSegmentRows) pl.size = 0;
+    if (pl.size > 0) {
+        if (!map2(enc, &p.a, x, K, rows, BK) || !map2(enc, &p.b[0], dy, N, rows, BK))
+            return moe::cuda_fail(cudaErrorInvalidValue);
+        p.features = (int)K;
+        p.cols = (int)N;
+        return launch_split<kWgrad, 128>(p, groups * ceil_div(N, 128) * ceil_div(K, kSplitF<kWgrad>), pl.size, stream);
+    }
+    if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK) ||
+        !out_map(enc, &p.c, dw, eb, K, N, groups))
+        return moe::cuda_fail(cudaErrorInvalidValue);
+    p.features = (int)N;
+    p.cols = (int)K;
+    return launch_kernel<kWgrad>(p, pairs, stream);
 }
 
 swiglu_status_t swiglu_grouped_timeout_flag(int *flag) {

@@ -119,7 +119,7 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&v)[32]) {
 // 16 TMEM lanes by 32 fp32 columns in the matrix-fragment layout: registers
 // 4j .. 4j + 3 of thread t hold columns 8j + 2 (t % 4) and the next one of lane
 // t / 4 (first two) and of lane t / 4 + 8.
-__device__ __forceinline__ void tmem_load_16x32(uint32_t taddr, uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_load_16x32(uint32_t taddr, uint32_t *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
