@@ -31,7 +31,7 @@
 //
 // The weight gradient's contraction runs over a group's rows, so its last block
 // of 64 would take in rows of the next group.  Those loads are counted on a
-// barrier of their own, warp 7 of each CTA zeroes the rows beyond the group in
+// barrier of their own, the last warp of each CTA zeroes the rows beyond the group in
 // shared memory (a product with 0 would not do: a neighbour's row may hold
 // NaN), and only then the stage is handed to the tensor cores.
 #include <climits>
@@ -63,7 +63,7 @@ constexpr int kGroupN = 16;          // N tiles per block of the tile order
 // are added with rounded fp32 additions
 constexpr int kSegmentRows = 4096;
 
-constexpr int kTileSlots = 3;        // tiles taken ahead, at most
+constexpr int kTileSlots = 2;
 // byte offsets in the region after the ring
 constexpr int OFF_FULL = 0;
 constexpr int OFF_EMPTY = OFF_FULL + 8 * STAGES;
@@ -80,15 +80,13 @@ constexpr int OFF_TMEM = OFF_TILE + 32 * kTileSlots;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
 constexpr int STATE_BYTES = 512;
 static_assert(OFF_ABORT + 4 <= STATE_BYTES, "barriers and state fit their region");
-// the epilogue's staging, per warp: buffers of 32 rows of 64 bytes for bulk
-// stores (64-byte swizzle); kFc1: 32 rows of 32 gates and 32 ups per pair of
-// warps, fp32, rows padded by 4 words
-constexpr int kBuffers = 3;
-constexpr int BUF_BYTES = 32 * 64;
-constexpr int STG_WARP_BYTES = kBuffers * BUF_BYTES;
-constexpr int STG_BYTES = 4 * STG_WARP_BYTES;
+// the epilogue's staging, per warp: 32 rows of 64 bytes for bulk stores (64-byte
+// swizzle); kFc1: 32 rows of 32 gates and 32 ups per pair of warps, fp32, rows
+// padded by 4 words
+constexpr int STG_WARP_BYTES = 32 * 64;
 constexpr int STG_ROW_FC1 = 68;
-static_assert(32 * STG_ROW_FC1 * 4 <= 2 * STG_WARP_BYTES, "a pair of warps has the room of two");
+constexpr int STG_PAIR_FC1 = 32 * STG_ROW_FC1 * 4;
+constexpr int STG_BYTES = 18 * 1024;
 constexpr int TABLE_BYTES = 2 * (kMaxGroups + 2) * 4;
 constexpr int SMEM_BYTES = RING_BYTES + STG_BYTES + STATE_BYTES + (TABLE_BYTES + 15) / 16 * 16 + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM");
@@ -305,10 +303,16 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int m, int 
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// Warps: 0 loads, 1 MMA, 2 - 5 epilogue, 6 scheduler, 7 (kWgrad) zeroes rows.
-constexpr int kScheduler = 6, kZeroWarp = 7;
+// Warps: 0 loads, 1 MMA, 2 .. epilogue, then the scheduler and (kWgrad) the warp
+// that zeroes rows.  The epilogue has four warps, one per quarter of the
+// accumulator's lanes, or eight, which take every other 32 columns each.
 template <int MODE>
-constexpr int kPairThreads = 32 * (MODE == kWgrad ? 8 : 7);
+constexpr int kEpiWarps = MODE == kFc1 ? 4 : 8;
+template <int MODE>
+constexpr int kScheduler = 2 + kEpiWarps<MODE>;
+template <int MODE>
+constexpr int kPairThreads = 32 * (3 + kEpiWarps<MODE> + (MODE == kWgrad ? 1 : 0));
+static_assert(8 * STG_WARP_BYTES <= STG_BYTES && 2 * STG_PAIR_FC1 <= STG_BYTES, "the epilogue's staging");
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 1)
@@ -335,7 +339,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
     constexpr bool kBMn = MODE == kWgrad;
     // readers of a tile: the MMA thread and, of both CTAs, the producer, the
     // epilogue warps and, for the weight gradient, the warp that zeroes rows
-    constexpr int kReaders = 1 + 2 * (1 + 4 + (MODE == kWgrad ? 1 : 0));
+    constexpr int kEpi = kEpiWarps<MODE>;
+    constexpr int kReaders = 1 + 2 * (1 + kEpi + (MODE == kWgrad ? 1 : 0));
 
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
@@ -345,14 +350,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             // kWgrad: an arrival for each CTA's half (both by the leader's producer,
-            // or warp 7 of each once the rows beyond the group are zero)
+            // or the last warp of each once the rows beyond the group are zero)
             mbar_init(full0 + 8 * s, MODE == kWgrad ? 2 : 1);
             mbar_init(empty0 + 8 * s, 1);
             mbar_init(tail0 + 8 * s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(acc_full0 + 8 * a, 1);
-            mbar_init(acc_empty0 + 8 * a, 8);
+            mbar_init(acc_empty0 + 8 * a, 2 * kEpi);
         }
         mbar_init(mma_done, 1);
         for (int i = 0; i < kTileSlots; ++i) {
@@ -413,37 +418,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
         return t;
     };
 
-    if (warp == kScheduler) {
-        // ---- scheduler (the leader's): takes tiles and publishes them to both
-        // CTAs, up to kTileSlots ahead of the slowest reader, so that neither the
-        // cancellation's latency nor finding a tile's group delays the loads
+    if (warp == kScheduler<MODE>) {
+        // ---- scheduler (the leader's): finds each tile's group and publishes it to
+        // both CTAs while the one before is worked on.  The next tile is that of a
+        // cluster whose launch it cancels, asked for once there is room for it: pairs
+        // that ran ahead of their loads would take the last tiles from the others.
         if (leader && elect_one()) {
             int tile = (int)(blockIdx.x >> 1), asks = 0;
-            // take another cluster's tile; -1 when no pending one was left
-            const auto take = [&]() {
-                mbar_arrive_expect_tx(clc_bar, 16);
-                clc_try_cancel(clc_resp, clc_bar);
-                if (!mbar_wait<true>(clc_bar, asks++ & 1)) return -1;
-                const int x = clc_cancelled_cta(clc_resp);
-                if (x < 0) return -1;
-                if ((x & 1) != 0 || x >= (int)gridDim.x) {  // not a cluster's first CTA of this grid
-                    *abort_flag = 1;
-                    atomicExch(&g_timeout, 1);
-                    return -1;
-                }
-                return x >> 1;
+            const auto next = [&]() {
+                do {
+                    mbar_arrive_expect_tx(clc_bar, 16);
+                    clc_try_cancel(clc_resp, clc_bar);
+                    if (!mbar_wait<true>(clc_bar, asks++ & 1)) return -1;
+                    const int x = clc_cancelled_cta(clc_resp);
+                    if (x < 0) return -1;  // no pending cluster was left
+                    if ((x & 1) != 0 || x >= (int)gridDim.x) {  // not a cluster's first CTA of this grid
+                        *abort_flag = 1;
+                        atomicExch(&g_timeout, 1);
+                        return -1;
+                    }
+                    tile = x >> 1;
+                } while (tile >= tiles);  // beyond the last tile
+                return tile;
             };
             for (int k = 0;; ++k) {
                 const int slot = k % kTileSlots;
-                while (tile >= tiles) tile = take();  // beyond the last tile
+                if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) *abort_flag = 1;
+                if (k > 0 || tile >= tiles) tile = *abort_flag ? -1 : next();
                 Tile t;
                 t.group = -1;
-                if (tile >= 0) t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
-                if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) *abort_flag = 1;
-                if (*abort_flag) t.group = -1;
+                if (tile >= 0 && !*abort_flag) t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
                 publish(tile0 + 32 * slot, tile_full0 + 8 * slot, t);
                 if (t.group < 0) break;
-                tile = take();
             }
         }
     } else if (warp == 0 && elect_one()) {
@@ -466,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                 const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
                 uint32_t bar = map_to_rank(full0 + 8 * s, 0);
                 if (MODE == kWgrad && (kb + 1) * BK > t.rows) {
-                    // rows beyond the group: warp 7 of each CTA hands its half on
+                    // rows beyond the group: the last warp of each CTA hands its half on
                     bar = map_to_rank(tail0 + 8 * s, rank);
                     mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
                 } else if (leader) {
@@ -567,20 +573,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
         }
         mma_commit_local_pair(mma_done);
         mbar_wait(mma_done, 0);
-    } else if (warp >= 2 && warp < 6) {
+    } else if (warp >= 2 && warp < 2 + kEpi) {
         // ---- epilogue (both CTAs): this CTA's 128 lanes of the accumulator,
         // a quarter per warp
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, set = (warp - 2) >> 2;
+        constexpr int kStep = 8 * kEpi;  // columns from one chunk of a warp to its next
         const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
-        float *stg_pair = reinterpret_cast<float *>(staging + (quarter >> 1) * (2 * STG_WARP_BYTES));
-        unsigned char *buffers = staging + quarter * STG_WARP_BYTES;
-        int buf = 0;
-        // the next buffer, once the bulk store that read it last is done with it
-        const auto next_buffer = [&]() {
-            buf = buf == kBuffers - 1 ? 0 : buf + 1;
-            if (elect_one()) bulk_wait_read<kBuffers - 1>();
+        float *stg_pair = reinterpret_cast<float *>(staging + (quarter >> 1) * STG_PAIR_FC1);
+        unsigned char *to = staging + (4 * set + quarter) * STG_WARP_BYTES;
+        // the buffer, once the bulk store that read it last is done with it
+        const auto free_buffer = [&]() {
+            if (elect_one()) bulk_wait_read<0>();
             __syncwarp();
-            return buffers + buf * BUF_BYTES;
         };
         const int bar_id = 1 + (quarter >> 1);
         int lt = 0;
@@ -612,8 +616,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                 const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
                 // (reading the next 32 columns ahead of storing these was no faster:
                 // 4.7 us per 256 x 256 tile of one contraction block against 4.3)
+                if (32 * set >= width) {  // no columns for this warp
+                    if (lane == 0) mbar_arrive_cluster(acc_empty_leader0 + 8 * acc);
+                    continue;
+                }
 #pragma unroll 1
-                for (int c = 0; c < width; c += 32) {
+                for (int c = 32 * set; c < width; c += kStep) {
                     uint32_t v[32];
                     if constexpr (MODE == kMm || MODE == kDgrad) {
                         tmem_load_16x32(tbase + c, v);  // lanes 0 - 15 and 16 - 31 of the quarter
@@ -622,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                         tmem_load32(tbase + c, v);
                     }
                     tmem_wait_ld();
-                    if (c + 32 >= width) {
+                    if (c + kStep >= width) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc_empty_leader0 + 8 * acc);
@@ -710,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                             const bool add = p.accumulate || !first;
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                unsigned char *to = next_buffer();
+                                free_buffer();
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     *reinterpret_cast<uint4 *>(to + lane * 64 + ((i ^ swz) << 4)) =
@@ -720,17 +728,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                                 __syncwarp();
                                 const bool in = row0 < p.features && t.n0 + c + 16 * h < p.cols;
                                 if (elect_one()) {
-                                    if (!in)
-                                        ;  // (the empty group keeps the count of the buffers)
-                                    else if (add)
+                                    if (in && add)
                                         tma_add_3d(&p.c, smem_addr(to), t.n0 + c + 16 * h, row0, t.group);
-                                    else
+                                    else if (in)
                                         tma_store_3d(&p.c, smem_addr(to), t.n0 + c + 16 * h, row0, t.group);
                                     bulk_commit();
                                 }
                             }
                         } else {
-                            unsigned char *to = next_buffer();
+                            free_buffer();
                             uint32_t w[16];
 #pragma unroll
                             for (int i = 0; i < 32; i += 2)
@@ -750,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                     } else {
                         // transposed on the way to shared memory: row r of the buffer
                         // is row c + r of the tile, its 16-byte pieces 8 features each
-                        unsigned char *to = next_buffer();
+                        free_buffer();
                         const uint32_t at = smem_addr(to) + (lane & 7) * 64 +
                                             (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
 #pragma unroll
@@ -776,7 +782,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                                 bulk_commit();
                             }
                         } else {  // the rows after these are another group's
-                            if (elect_one()) bulk_commit();  // (an empty group: next_buffer counts them)
                             __syncwarp();
                             const int f = col + 8 * (lane & 3);
 #pragma unroll
@@ -794,7 +799,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
             } while (kb < kblocks);
         }
         if (elect_one()) bulk_wait<0>();  // the stores, before their shared memory goes
-    } else if (MODE == kWgrad && warp == kZeroWarp) {
+    } else if (MODE == kWgrad && warp == kScheduler<MODE> + 1) {
         // ---- zero the rows beyond the group in its last stage (both CTAs)
         int it = 0;
         uint32_t uses = 0;  // phase of each stage's tail barrier
@@ -875,6 +880,50 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return n;
 }
 
+// First block of slice s of `blocks` blocks cut into `size` (a power of two) slices.
+__device__ __forceinline__ int slice_begin(int blocks, uint32_t s, uint32_t size) {
+    return (int)(((uint64_t)(uint32_t)blocks * s) >> (31 - __clz((int)size)));
+}
+
+// R rows of four features summed over up to SL slices in rank order, every load
+// issued before the first is used (a load from another SM takes long).  `from`:
+// this CTA's address of the first row's features (the ups of kFc1 32 lanes on);
+// `step`: rows from one to the next; `rows`: how many there are; bit s of `have`:
+// slice s has a part.
+template <int MODE, int R, int SL>
+__device__ __forceinline__ void join_rows(uint32_t from, int step, int rows, uint32_t have, float (&g)[R][4],
+                                          float (&u)[R][4]) {
+    float4 a[R][SL], b[R][SL];
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+        if (!(have >> s & 1)) continue;
+        const uint32_t at = map_to_rank(from, (uint32_t)s);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (i < rows) {
+                a[i][s] = ld_cluster(at + (uint32_t)(i * step * kPartialRow) * 4);
+                if (MODE == kFc1) b[i][s] = ld_cluster(at + (uint32_t)(i * step * kPartialRow + 32) * 4);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) g[i][x] = u[i][x] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+            if (i < rows && (have >> s & 1)) {
+                g[i][0] = __fadd_rn(g[i][0], a[i][s].x), g[i][1] = __fadd_rn(g[i][1], a[i][s].y);
+                g[i][2] = __fadd_rn(g[i][2], a[i][s].z), g[i][3] = __fadd_rn(g[i][3], a[i][s].w);
+                if (MODE == kFc1) {
+                    u[i][0] = __fadd_rn(u[i][0], b[i][s].x), u[i][1] = __fadd_rn(u[i][1], b[i][s].y);
+                    u[i][2] = __fadd_rn(u[i][2], b[i][s].z), u[i][3] = __fadd_rn(u[i][3], b[i][s].w);
+                }
+            }
+        }
+    }
+}
+
 template <int MODE, int NT>
 __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(const __grid_constant__ Params p) {
     extern __shared__ unsigned char smem_raw[];
@@ -932,8 +981,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
         t = tile_at<MODE, kSplitF<MODE>, NT, 16>(p, groups, tile);
         if (t.group != p.groups) {
             const int kblocks = ((MODE == kWgrad ? t.rows : p.depth) + BK - 1) / BK;
-            kb0 = (int)((int64_t)kblocks * rank / size);
-            kb1 = (int)((int64_t)kblocks * (rank + 1) / size);
+            kb0 = slice_begin(kblocks, rank, size);
+            kb1 = slice_begin(kblocks, rank + 1, size);
         }
     }
     const int width = (t.cnt + 15) / 16 * 16;
@@ -1039,59 +1088,44 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
     if (size > 1) cluster_sync();
     if (live) {
         // rows rank, rank + S, ... of the tile: 16 (kFc1) or 32 threads a row, four
-        // features each, summed over the slices in rank order; kAtOnce rows of a
-        // thread in flight, as a load from another SM takes long
+        // features each; a few rows at once of up to two slices, or one of up to eight
         constexpr int kRowThreads = kSplitF<MODE> / 4;
         constexpr int kPass = kSplitThreads / kRowThreads;  // rows of the CTA per pass
-        constexpr int kAtOnce = 4;
         static_assert(kSplitThreads % kRowThreads == 0, "whole rows of threads");
         uint32_t have = 0;  // slices with a block (a short group of kWgrad leaves some without)
         if (t.group != p.groups) {
             const int blocks = ((MODE == kWgrad ? t.rows : p.depth) + BK - 1) / BK;
             for (uint32_t s = 0; s < size; ++s)
-                if ((int64_t)blocks * s / size < (int64_t)blocks * (s + 1) / size) have |= 1u << s;
+                if (slice_begin(blocks, s, size) < slice_begin(blocks, s + 1, size)) have |= 1u << s;
         }
         const int f = (int)threadIdx.x % kRowThreads;
         // kFc1: 32 gates, 32 ups, 32 gates, 32 ups
         const int lane0 = MODE == kFc1 ? f / 8 * 64 + f % 8 * 4 : f * 4;
         const int col = t.m0 + 4 * f;
         const int step = kPass * (int)size;
+        constexpr int kRows = MODE == kFc1 ? 2 : 4;
+        const int at_once = size <= 2 ? kRows : 1;
         // (the trip counts are the same for a whole warp: the block maximum is shuffled)
-        for (int r0 = (int)rank; r0 < t.cnt; r0 += kAtOnce * step) {
+        for (int r0 = (int)rank; r0 < t.cnt; r0 += at_once * step) {
             const int first = r0 + (int)(threadIdx.x / kRowThreads) * (int)size;
-            float gs[kAtOnce][4] = {}, us[MODE == kFc1 ? kAtOnce : 1][4] = {};
-            if (col < p.features) {
-                for (uint32_t s = 0; s < size; ++s) {
-                    if (!(have >> s & 1)) continue;
-                    const uint32_t from = map_to_rank(ring + (uint32_t)(first * kPartialRow + lane0) * 4, s);
-                    float4 a[kAtOnce], b[kAtOnce];
+            const int rows = col < p.features && first < t.cnt ? (t.cnt - first + step - 1) / step : 0;
+            const uint32_t from = ring + (uint32_t)(first * kPartialRow + lane0) * 4;
+            float gs[kRows][4], us[kRows][4];
+            if (size <= 2) {
+                join_rows<MODE, kRows, 2>(from, step, rows, have, gs, us);
+            } else {
+                float g1[1][4], u1[1][4];
+                join_rows<MODE, 1, 8>(from, step, rows, have, g1, u1);
 #pragma unroll
-                    for (int i = 0; i < kAtOnce; ++i) {
-                        if (first + i * step < t.cnt) {
-                            a[i] = ld_cluster(from + (uint32_t)(i * step * kPartialRow) * 4);
-                            if (MODE == kFc1) b[i] = ld_cluster(from + (uint32_t)(i * step * kPartialRow + 32) * 4);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kAtOnce; ++i) {
-                        if (first + i * step < t.cnt) {
-                            gs[i][0] = __fadd_rn(gs[i][0], a[i].x), gs[i][1] = __fadd_rn(gs[i][1], a[i].y);
-                            gs[i][2] = __fadd_rn(gs[i][2], a[i].z), gs[i][3] = __fadd_rn(gs[i][3], a[i].w);
-                            if constexpr (MODE == kFc1) {
-                                us[i][0] = __fadd_rn(us[i][0], b[i].x), us[i][1] = __fadd_rn(us[i][1], b[i].y);
-                                us[i][2] = __fadd_rn(us[i][2], b[i].z), us[i][3] = __fadd_rn(us[i][3], b[i].w);
-                            }
-                        }
-                    }
-                }
+                for (int x = 0; x < 4; ++x) gs[0][x] = g1[0][x], us[0][x] = u1[0][x];
             }
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                if (r0 + i * step >= t.cnt) break;
+            for (int i = 0; i < kRows; ++i) {
+                if (i >= at_once || r0 + i * step >= t.cnt) break;
                 const int r = first + i * step;
                 const bool in = r < t.cnt && col < p.features;
                 float(&g)[4] = gs[i];
-                float(&u)[4] = us[MODE == kFc1 ? i : 0];
+                float(&u)[4] = us[i];
                 const int64_t row = (int64_t)t.r0 + t.n0 + r;
                 const auto pack = [](const float (&v)[4], uint32_t (&w)[2]) {
                     swiglu::BF16::put2(w, 0, v[0], v[1]);
@@ -1176,6 +1210,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
 
 // ---------------------------------------------------------------- host side
 
+namespace {
+
 // A bf16 tensor of `rank` dimensions, innermost first, dense in every row, as
 // boxes of 64 elements of the innermost dimension (128 bytes) with the matching
 // swizzle; zero fill outside.
@@ -1227,8 +1263,13 @@ bool row_maps(EncodeTiled enc, CUtensorMap *maps, const void *p, int64_t inner, 
     return true;
 }
 
+constexpr int kSms = 152;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// One cluster per tile, of which there are `clusters` at most.
 template <int MODE>
-swiglu_status_t launch_kernel(const Params &p, int64_t clusters, swiglu_stream_t stream) {
+swiglu_status_t launch_pairs(const Params &p, int64_t clusters, swiglu_stream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return moe::cuda_fail(e);
@@ -1271,41 +1312,38 @@ swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_st
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
 
-// Pairs or split?  Both kernels are bound by the operand bytes that an SM takes
-// in (about 100 GB/s were seen), so the rule compares, per block of depth, the
-// bytes of a CTA's stage times the rounds that its grid takes on the 152 SMs.
-// It counts the tiles of groups of equal size, which is all the host knows.  The
-// split kernel's least cost over S adds the other constants: times as bytes at
-// that rate (100 KiB: 1 us).
+// Pairs or split?  The rule estimates both times in nanoseconds from the tiles of
+// groups of equal size, which is all the host knows: operand bytes per SM at the
+// rates the two kernels reach, times the rounds of the grid, plus what a launch,
+// a tile and the joining of the sums take.  The constants are a fit to the times
+// of all five choices on 7,600 shapes (forward, fc1 and both gradients; 1 to
+// 32768 rows, 1 to 64 groups, widths 64 to 14336); with them the choice is on
+// average 2.9 % slower than the best one, where always pairs are 22 % and always
+// one CTA per tile 31 % slower.
 struct Plan {
     int size;  // CTAs per tile of the split kernel; 0: pairs
 };
-constexpr int kSms = 152;
-constexpr int64_t kJoin = 100 * 1024;
-constexpr int64_t kPairs = 500 * 1024;      // the pairs' way in and out
-constexpr int64_t kPairTile = 430 * 1024;   // a pair's tile at least: its epilogue
-constexpr int64_t kSplitTile = 300 * 1024;  // a CTA's way in and out, once per tile
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// `rows_per`: N extent of a group's tiles (rows, or columns of dW); `same`: groups
-// with that extent; features: the M extent; pair_f / split_f: features of a tile.
-Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int split_f, int nt, int64_t kblocks) {
+// `same` groups of `rows_per` rows (kWgrad: of dW's columns) by `features`; pair_f
+// and split_f: features of a tile, nt: rows of a tile of the split kernel;
+// least_size: the fewest slices a sum may be cut into (pairs cut it themselves).
+Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int split_f, int nt, int64_t kblocks,
+          int64_t least_size = 1) {
     const int64_t pair_n = rows_per < TILE_N ? ceil_div(rows_per, 32) * 32 : TILE_N;
     const int64_t pair_tiles = same * ceil_div(rows_per, TILE_N) * ceil_div(features, pair_f);
-    const int64_t pair_depth = kblocks * (A_BYTES + pair_n * BK);
-    const int64_t pair_cost =
-        ceil_div(pair_tiles, kSms / 2) * (pair_depth > kPairTile ? pair_depth : kPairTile) + kPairs;
+    const int64_t pair_depth = kblocks * (A_BYTES + pair_n * BK) / 111;
+    Plan best = {0};
+    int64_t least = ceil_div(pair_tiles, kSms / 2) * (pair_depth > 1590 ? pair_depth : 1590) + 5570;
     const int64_t split_n = rows_per < nt ? ceil_div(rows_per, 16) * 16 : nt;
     const int64_t split_tiles = same * ceil_div(rows_per, nt) * ceil_div(features, split_f);
-    Plan best = {0};
-    int64_t least = pair_cost;
     for (int size = 1; size <= 8 && (size == 1 || 2 * size <= kblocks); size *= 2) {
-        const int64_t cost = ceil_div(split_tiles * size, kSms) *
-                                 (ceil_div(kblocks, size) * (A_BYTES + split_n * BK * 2) + kSplitTile) +
-                             (size > 1 ? kJoin : 0);
-        if (cost < least) {
-            least = cost;
+        if (size < least_size) continue;
+        const int64_t ctas = split_tiles * size;
+        const int64_t bytes = ceil_div(kblocks, size) * (A_BYTES + split_n * BK * 2);
+        const int64_t time = (ctas <= kSms ? bytes / 102 : ceil_div(ctas, kSms) * bytes / 123) +
+                             ceil_div(ctas, 2 * kSms) * (3750 + 20 * split_n / size) + (size > 1 ? 1090 : 0);
+        if (time < least) {
+            least = time;
             best.size = size;
         }
     }
@@ -1322,7 +1360,7 @@ swiglu_status_t launch_rows(const Params &p, swiglu_stream_t stream) {
     const Plan pl = plan(same, ceil_div(p.rows, same), p.features, kTileF<MODE>, kSplitF<MODE>, few ? 32 : 128,
                          ceil_div(p.depth, BK));
     const int64_t tiles = most_tiles(p.rows, p.groups, p.features, kSplitF<MODE>, few ? 32 : 128);
-    if (pl.size == 0 || tiles > INT32_MAX / 16) return launch_kernel<MODE>(p, pairs, stream);
+    if (pl.size == 0 || tiles > INT32_MAX / 16) return launch_pairs<MODE>(p, pairs, stream);
     return few ? launch_split<MODE, 32>(p, tiles, pl.size, stream) : launch_split<MODE, 128>(p, tiles, pl.size, stream);
 }
 
@@ -1341,6 +1379,8 @@ bool aligned(std::initializer_list<const void *> ps, uintptr_t by) {
         if ((uintptr_t)p % by != 0) return false;
     return true;
 }
+
+}  // namespace
 
 }  // namespace gmm
 
@@ -1489,8 +1529,8 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     p.accumulate = accumulate != 0;
     // Pairs: M is dW's rows, N its columns.  Split: the other way round, so that the
     // lanes run along dW's rows; an fp32 sum's slices stay within a segment.
-    Plan pl = plan(groups, N, K, 256, kSplitF<kWgrad>, 128, ceil_div(ceil_div(rows, groups), BK));
-    if (p.f32_out && rows / (pl.size > 0 ? pl.size : 1) > kSegmentRows) pl.size = 0;
+    const Plan pl = plan(groups, N, K, 256, kSplitF<kWgrad>, 128, ceil_div(ceil_div(rows, groups), BK),
+                         p.f32_out ? ceil_div(rows, kSegmentRows) : 1);
     if (pl.size > 0) {
         if (!map2(enc, &p.a, x, K, rows, BK) || !map2(enc, &p.b[0], dy, N, rows, BK))
             return moe::cuda_fail(cudaErrorInvalidValue);
@@ -1503,7 +1543,7 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
         return moe::cuda_fail(cudaErrorInvalidValue);
     p.features = (int)N;
     p.cols = (int)K;
-    return launch_kernel<kWgrad>(p, pairs, stream);
+    return launch_pairs<kWgrad>(p, pairs, stream);
 }
 
 swiglu_status_t swiglu_grouped_timeout_flag(int *flag) {
