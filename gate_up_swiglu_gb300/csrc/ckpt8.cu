@@ -31,8 +31,20 @@ bool multiple(int64_t by, std::initializer_list<int64_t> v) {
     return true;
 }
 
+// Packs a thread of the forward takes at once, by the pack's bytes.
+template <int BYTES>
+constexpr int kFwdPacks = BYTES >= 32 ? 1 : 2;
+
 // Blocks of 32 columns a warp of the single-element kernels takes at a time.
 constexpr int kNarrowFwd = 8, kNarrowBwd = 4;
+
+// The weighted backward: packs (or groups of four elements) of a row that one
+// warp takes ([16384, 2 x 256] bf16 22 -> 12 us against a CTA per row), and the
+// CTAs up to which rows are shared by clusters (one row of n = 28008 fp32 23 -> 9 us).
+// 16-byte packs take CTAs of 256 threads ([8192, 2 x 14344] bf16 175 -> 153 us; 32-byte
+// packs of n = 14336 were slower that way, 144 -> 159 us).
+constexpr int64_t kWarpRow = 64;
+constexpr int64_t kClusterCtas = 152 * 8;
 
 // CTAs of T threads for `packs` packs, one pack a thread (the kernels' grid
 // stride covers what the launch limit leaves).
@@ -55,7 +67,8 @@ swiglu_status_t launch_fwd(ckpt8::FwdParams p, swiglu_stream_t stream) {
         p.row_packs = p.blocks * (ckpt8::kBlock / VEC);
         p.packs = p.rows * p.row_packs;
         p.div = make_fast_div((uint64_t)p.row_packs);
-        e = moe::launch(ckpt8::ckpt8_fwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, 0, p);
+        constexpr int U = kFwdPacks<E::kBytes * VEC>;
+        e = moe::launch(ckpt8::ckpt8_fwd_kernel<E, VEC, U, T>, dim3(one_pass(p.packs, U * T)), T, 0, stream, 0, p);
     }
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
@@ -68,8 +81,21 @@ swiglu_status_t launch_bwd(ckpt8::BwdParams p, swiglu_stream_t stream) {
     p.div = make_fast_div((uint64_t)p.row_packs);
     cudaError_t e;
     if (p.dw != nullptr) {
-        const unsigned grid = (unsigned)(p.rows < INT32_MAX ? p.rows : INT32_MAX);
-        e = moe::launch(ckpt8::ckpt8_bwd_weighted_kernel<E, VEC, T>, dim3(grid), T, 0, stream, 0, p);
+        // a warp per row of up to kWarpRow packs, else a CTA, or a cluster while that
+        // gives the SMs more to do
+        const int64_t packs = VEC == 1 ? (p.n + 3) / 4 : p.row_packs;
+        if (packs <= kWarpRow) {
+            const int64_t ctas = (p.rows + T / 32 - 1) / (T / 32);
+            e = moe::launch(ckpt8::ckpt8_bwd_weighted_kernel<E, VEC, T, T / 32>,
+                            dim3((unsigned)(ctas < INT32_MAX ? ctas : INT32_MAX)), T, 0, stream, 0, p);
+        } else {
+            int size = 1;
+            while (size < 8 && p.rows * size * 2 <= kClusterCtas && packs > (int64_t)T * size) size *= 2;
+            const int64_t ctas = p.rows < (1 << 27) ? p.rows : (1 << 27);
+            constexpr int TR = E::kBytes * VEC == 16 ? 256 : T;
+            e = moe::launch(ckpt8::ckpt8_bwd_weighted_kernel<E, VEC, TR, 1>, dim3((unsigned)(ctas * size)), TR, 0,
+                            stream, size, p);
+        }
     } else if constexpr (VEC == 1) {
         constexpr int K = kNarrowBwd;
         p.row_packs = (int32_t)((p.n + 32 * K - 1) / (32 * K));

@@ -101,7 +101,9 @@ __device__ __forceinline__ void decode(const uint32_t *q, float f, float *v) {
 // writes y, two codes and 2/32 scale bytes; the backward reads dy, the codes
 // and scales and writes dx (and y).  In bf16 that is 8.06 bytes a pair either
 // way for about 15 (forward) and 20 (backward) instructions, so both are bound
-// by HBM.
+// by HBM: [8192, 2 x 14336] bf16 forward 150 us (0.95 of the 6680 GB/s copy),
+// backward without weights 140 us (1.01; 169 us with y, 1.05), fp32
+// [8192, 2 x 4096] 72 / 71 us (0.98 / 0.99).
 //
 // A pack is VEC elements of one half; a block of 32 columns is 32 / VEC
 // neighbouring lanes, so the forward's block maximum is a shuffle inside that
@@ -124,7 +126,10 @@ struct FwdParams {
     int32_t blocks;              // per half
 };
 
-template <typename E, int VEC, int T>
+// U packs per thread, T packs apart, all loaded first: 1 for 32-byte packs (two:
+// 172 us against 150 for [8192, 2 x 14336] bf16), 2 for 16-byte packs (one: 186 us
+// against 175 for [8192, 2 x 14344]).  CTAs of 256 or 64 threads were no faster.
+template <typename E, int VEC, int U, int T>
 __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
     swiglu::await_previous_grid();
     swiglu::allow_next_grid();
@@ -133,53 +138,63 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
     constexpr int kLanes = kBlock / VEC;  // lanes of a block
     constexpr int QW = (VEC + 3) / 4;
     // the loop's condition is the same for a whole warp: the shuffles need it
-    for (int64_t v0 = (int64_t)blockIdx.x * T + (threadIdx.x & ~31); v0 < p.packs; v0 += (int64_t)gridDim.x * T) {
-        const int64_t v = v0 + (threadIdx.x & 31);
-        const int64_t r = swiglu::fast_div(v, p.div);
-        const int32_t c = (int32_t)(v - r * p.row_packs);
-        const int64_t col = (int64_t)c * VEC;
-        const bool live = v < p.packs && col < p.n;
-        uint32_t gw[NW] = {}, uw[NW] = {};
-        float wr = 1.0f;
-        if (live) {
-            const char *xr = p.x + r * p.x_stride + col * E::kBytes;
-            swiglu::Ld<B, swiglu::kLdNC>::run(xr, gw);
-            swiglu::Ld<B, swiglu::kLdNC>::run(xr + p.n * E::kBytes, uw);
-            if (p.w != nullptr) wr = __ldg(p.w + r);
-        }
-        float g[VEC], u[VEC];
+    for (int64_t v0 = (int64_t)blockIdx.x * (U * T) + (threadIdx.x & ~31); v0 < p.packs;
+         v0 += (int64_t)gridDim.x * (U * T)) {
+        uint32_t gw[U][NW], uw[U][NW];
+        int64_t row[U];
+        int32_t col[U];  // first column (n <= 2^30); -1: no pack
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            g[i] = E::get(gw, i);
-            u[i] = E::get(uw, i);
-        }
-        float mg = finite_amax<VEC>(g), mu = finite_amax<VEC>(u);
+        for (int k = 0; k < U; ++k) {
+            const int64_t v = v0 + (threadIdx.x & 31) + k * T;
+            row[k] = swiglu::fast_div(v, p.div);
+            const int32_t c = (int32_t)(v - row[k] * p.row_packs);
+            col[k] = v < p.packs && (int64_t)c * VEC < p.n ? c * VEC : -1;
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) {
-            mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-            mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+            for (int i = 0; i < NW; ++i) gw[k][i] = uw[k][i] = 0u;
+            if (col[k] >= 0) {
+                const char *xr = p.x + row[k] * p.x_stride + (int64_t)col[k] * E::kBytes;
+                swiglu::Ld<B, swiglu::kLdNC>::run(xr, gw[k]);
+                swiglu::Ld<B, swiglu::kLdNC>::run(xr + p.n * E::kBytes, uw[k]);
+            }
         }
-        if (!live) continue;
-        const uint32_t cg = scale_code(mg), cu = scale_code(mu);
-        uint32_t qg[QW], qu[QW];
-        encode<VEC>(g, encode_factor(cg), qg);
-        encode<VEC>(u, encode_factor(cu), qu);
-        uint8_t *qr = p.q + r * p.q_stride + col;
-        swiglu::St<VEC, swiglu::kStStream>::run(qr, qg);
-        swiglu::St<VEC, swiglu::kStStream>::run(qr + p.n, qu);
-        if (c % kLanes == 0) {
-            uint8_t *sr = p.scales + r * p.s_stride + c / kLanes;
-            sr[0] = (uint8_t)cg;
-            sr[p.blocks] = (uint8_t)cu;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            float g[VEC], u[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                g[i] = E::get(gw[k], i);
+                u[i] = E::get(uw[k], i);
+            }
+            float mg = finite_amax<VEC>(g), mu = finite_amax<VEC>(u);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) {
+                mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+                mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+            }
+            if (col[k] >= 0) {
+                const uint32_t cg = scale_code(mg), cu = scale_code(mu);
+                uint32_t qg[QW], qu[QW];
+                encode<VEC>(g, encode_factor(cg), qg);
+                encode<VEC>(u, encode_factor(cu), qu);
+                uint8_t *qr = p.q + row[k] * p.q_stride + col[k];
+                swiglu::St<VEC, swiglu::kStStream>::run(qr, qg);
+                swiglu::St<VEC, swiglu::kStStream>::run(qr + p.n, qu);
+                if (col[k] % kBlock == 0) {
+                    uint8_t *sr = p.scales + row[k] * p.s_stride + col[k] / kBlock;
+                    sr[0] = (uint8_t)cg;
+                    sr[p.blocks] = (uint8_t)cu;
+                }
+                const float wr = p.w != nullptr ? __ldg(p.w + row[k]) : 1.0f;
+                float yv[VEC];
+                if (swiglu::pack_has_deep<E, VEC>(gw[k]))
+                    swiglu::fwd_pack<E, VEC, swiglu::kWeight, true>(gw[k], uw[k], nullptr, nullptr, wr, yv);
+                else
+                    swiglu::fwd_pack<E, VEC, swiglu::kWeight, false>(gw[k], uw[k], nullptr, nullptr, wr, yv);
+                uint32_t o[NW] = {};
+                swiglu::store_pack<E, VEC>(o, yv);
+                swiglu::St<B, swiglu::kStStream>::run(p.y + row[k] * p.y_stride + (int64_t)col[k] * E::kBytes, o);
+            }
         }
-        float yv[VEC];
-        if (swiglu::pack_has_deep<E, VEC>(gw))
-            swiglu::fwd_pack<E, VEC, swiglu::kWeight, true>(gw, uw, nullptr, nullptr, wr, yv);
-        else
-            swiglu::fwd_pack<E, VEC, swiglu::kWeight, false>(gw, uw, nullptr, nullptr, wr, yv);
-        uint32_t o[NW] = {};
-        swiglu::store_pack<E, VEC>(o, yv);
-        swiglu::St<B, swiglu::kStStream>::run(p.y + r * p.y_stride + col * E::kBytes, o);
     }
 }
 
@@ -188,8 +203,10 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
 // element.  A warp takes K blocks of 32 columns of one row, one lane per column,
 // so a block's maximum is one warp-wide reduction, each lane forms its row
 // pointers once for K elements, and all loads are issued before the first is
-// used.  (One element per thread over the flattened index, with shuffles for the
-// maximum, took 131 us for the forward of [3000, 2 x 5503] fp32 with weights.)
+// used: [3000, 2 x 5503] fp32 with weights forward 56 us (0.62 of copy; one element
+// per thread over the flattened index, with shuffles for the maximum, 131 us),
+// backward 56 us.  The memory instructions bound it: seven per 32 pairs, of 32 to
+// 128 bytes each, however few the others (bf16 [8192, 2 x 5503] 132 us, 0.41).
 
 // Positions of a warp: its row and the first column of its lane.
 struct Segment {
@@ -202,10 +219,20 @@ __device__ __forceinline__ Segment segment_at(int64_t seg, int32_t chunks, const
     return {r, (seg - r * chunks) * (32 * K) + (threadIdx.x & 31)};
 }
 
-// Bits of |v|, 0 unless finite: as integers they order like the values.
-__device__ __forceinline__ uint32_t finite_bits(float v) {
+// The scale code of the warp's 32 values (a block), from the bits of |v|, which
+// order like the values; `plain`: none is infinite, NaN or above 1.75 * 2^127, so
+// that encoding needs no care.
+struct BlockCode {
+    uint32_t code;
+    bool plain;
+};
+
+__device__ __forceinline__ BlockCode warp_code(float v) {
     const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
-    return b < 0x7f800000u ? b : 0u;
+    uint32_t m = __reduce_max_sync(0xffffffffu, b);
+    const bool plain = m <= 0x7f600000u;
+    if (!plain) m = __reduce_max_sync(0xffffffffu, b < 0x7f800000u ? b : 0u);
+    return {scale_code(__uint_as_float(m)), plain};
 }
 
 // p.row_packs: warps (segments of 32 K columns) per row; p.packs: in all.
@@ -238,14 +265,18 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_narrow_kernel(const FwdParams p) 
         for (int i = 0; i < K; ++i) {
             if (first + 32 * i >= p.n) break;  // the same for the whole warp
             const float gf = E::get(&g[i], 0), uf = E::get(&u[i], 0);
-            const uint32_t cg = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, finite_bits(gf))));
-            const uint32_t cu = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, finite_bits(uf))));
+            const BlockCode cg = warp_code(gf), cu = warp_code(uf);
+            const float fg = encode_factor(cg.code), fu = encode_factor(cu.code);
             if (i < live) {
-                uint32_t qg, qu;
-                encode<1>(&gf, encode_factor(cg), &qg);
-                encode<1>(&uf, encode_factor(cu), &qu);
-                qr[i * 32] = (uint8_t)qg;
-                qr[p.n + i * 32] = (uint8_t)qu;
+                uint32_t q = codes2(__fmul_rn(gf, fg), __fmul_rn(uf, fu));
+                if (!(cg.plain && cu.plain)) {
+                    uint32_t qg, qu;
+                    encode<1>(&gf, fg, &qg);
+                    encode<1>(&uf, fu, &qu);
+                    q = qg | qu << 8;
+                }
+                qr[i * 32] = (uint8_t)q;
+                qr[p.n + i * 32] = (uint8_t)(q >> 8);
                 const swiglu::Act act = swiglu::activation<E, false, true>(gf);
                 const float y = __fmul_rn(__fmul_rn(__fmul_rn(act.silu, uf), wr), act.scale);
                 uint32_t o = 0u;
@@ -253,8 +284,8 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_narrow_kernel(const FwdParams p) 
                 swiglu::St<EB, swiglu::kStStream>::run(yr + i * 32 * EB, &o);
             }
             if ((threadIdx.x & 31) == 0) {
-                sr[i] = (uint8_t)cg;
-                sr[i + p.blocks] = (uint8_t)cu;
+                sr[i] = (uint8_t)cg.code;
+                sr[i + p.blocks] = (uint8_t)cu.code;
             }
         }
     }
@@ -305,41 +336,48 @@ __device__ __forceinline__ void bwd_values(const uint32_t *d, const float *g, co
     }
 }
 
-template <typename E, int VEC, int MODE>
-__device__ __forceinline__ void bwd_one(const BwdParams &p, int64_t r, int32_t c, float wr, float &acc) {
-    constexpr int B = E::kBytes * VEC;
-    constexpr int NW = (B + 3) / 4;
-    constexpr int QW = (VEC + 3) / 4;
-    const int64_t col = (int64_t)c * VEC;
-    uint32_t d[NW], qg[QW], qu[QW];
-    const uint8_t *qr = p.q + r * p.q_stride + col;
-    const uint8_t *sr = p.scales + r * p.s_stride + col / kBlock;
-    swiglu::Ld<B, swiglu::kLdNC>::run(p.dy + r * p.dy_stride + col * E::kBytes, d);
-    swiglu::Ld<VEC, swiglu::kLdNC>::run(qr, qg);
-    swiglu::Ld<VEC, swiglu::kLdNC>::run(qr + p.n, qu);
-    const uint32_t cg = __ldg(sr), cu = __ldg(sr + p.blocks);
-    float g[VEC], u[VEC], dg[VEC], du[VEC], yv[VEC];
-    decode<VEC>(qg, decode_factor(cg), g);
-    decode<VEC>(qu, decode_factor(cu), u);
-    float gmin = g[0];
-#pragma unroll
-    for (int i = 1; i < VEC; ++i) gmin = fminf(gmin, g[i]);
-    if (E::kDeepScale && gmin < -64.0f)
-        bwd_values<E, VEC, MODE, true>(d, g, u, wr, acc, dg, du, yv);
-    else
-        bwd_values<E, VEC, MODE, false>(d, g, u, wr, acc, dg, du, yv);
-    uint32_t og[NW] = {}, ou[NW] = {};
-    swiglu::store_pack<E, VEC>(og, dg);
-    swiglu::store_pack<E, VEC>(ou, du);
-    char *dxr = p.dx + r * p.dx_stride + col * E::kBytes;
-    swiglu::St<B, swiglu::kStStream>::run(dxr, og);
-    swiglu::St<B, swiglu::kStStream>::run(dxr + p.n * E::kBytes, ou);
-    if (p.y != nullptr) {
-        uint32_t oy[NW] = {};
-        swiglu::store_pack<E, VEC>(oy, yv);
-        swiglu::St<B, swiglu::kStStream>::run(p.y + r * p.y_stride + col * E::kBytes, oy);
+// What a pack reads.
+template <typename E, int VEC>
+struct BwdPack {
+    static constexpr int B = E::kBytes * VEC;
+    uint32_t d[(B + 3) / 4], qg[(VEC + 3) / 4], qu[(VEC + 3) / 4], cg, cu;
+
+    __device__ __forceinline__ void load(const BwdParams &p, int64_t r, int32_t c) {
+        const int64_t col = (int64_t)c * VEC;
+        const uint8_t *qr = p.q + r * p.q_stride + col;
+        const uint8_t *sr = p.scales + r * p.s_stride + col / kBlock;
+        swiglu::Ld<B, swiglu::kLdNC>::run(p.dy + r * p.dy_stride + col * E::kBytes, d);
+        swiglu::Ld<VEC, swiglu::kLdNC>::run(qr, qg);
+        swiglu::Ld<VEC, swiglu::kLdNC>::run(qr + p.n, qu);
+        cg = __ldg(sr);
+        cu = __ldg(sr + p.blocks);
     }
-}
+
+    template <int MODE>
+    __device__ __forceinline__ void finish(const BwdParams &p, int64_t r, int32_t c, float wr, float &acc) const {
+        const int64_t col = (int64_t)c * VEC;
+        float g[VEC], u[VEC], dg[VEC], du[VEC], yv[VEC];
+        decode<VEC>(qg, decode_factor(cg), g);
+        decode<VEC>(qu, decode_factor(cu), u);
+        float gmin = g[0];
+#pragma unroll
+        for (int i = 1; i < VEC; ++i) gmin = fminf(gmin, g[i]);
+        if (E::kDeepScale && gmin < -64.0f)
+            bwd_values<E, VEC, MODE, true>(d, g, u, wr, acc, dg, du, yv);
+        else
+            bwd_values<E, VEC, MODE, false>(d, g, u, wr, acc, dg, du, yv);
+        uint32_t o[(B + 3) / 4] = {};
+        swiglu::store_pack<E, VEC>(o, dg);
+        char *dxr = p.dx + r * p.dx_stride + col * E::kBytes;
+        swiglu::St<B, swiglu::kStStream>::run(dxr, o);
+        swiglu::store_pack<E, VEC>(o, du);
+        swiglu::St<B, swiglu::kStStream>::run(dxr + p.n * E::kBytes, o);
+        if (p.y != nullptr) {
+            swiglu::store_pack<E, VEC>(o, yv);
+            swiglu::St<B, swiglu::kStStream>::run(p.y + r * p.y_stride + col * E::kBytes, o);
+        }
+    }
+};
 
 // Without weights: the flattened pack index, one pack per thread.
 template <typename E, int VEC, int T>
@@ -349,7 +387,10 @@ __global__ void __launch_bounds__(T) ckpt8_bwd_kernel(const BwdParams p) {
     float acc = 0.0f;
     for (int64_t v = (int64_t)blockIdx.x * T + threadIdx.x; v < p.packs; v += (int64_t)gridDim.x * T) {
         const int64_t r = swiglu::fast_div(v, p.div);
-        bwd_one<E, VEC, swiglu::kPlain>(p, r, (int32_t)(v - r * p.row_packs), 1.0f, acc);
+        const int32_t c = (int32_t)(v - r * p.row_packs);
+        BwdPack<E, VEC> pack;
+        pack.load(p, r, c);
+        pack.template finish<swiglu::kPlain>(p, r, c, 1.0f, acc);
     }
 }
 
@@ -379,9 +420,10 @@ __device__ __forceinline__ void bwd_elements(const BwdParams &p, const Segment &
 #pragma unroll
     for (int i = 0; i < K; ++i) {
         if (i < live) {
-            float g, u, dg, du, y;
-            decode<1>(&qg[i], decode_factor(cg[i]), &g);
-            decode<1>(&qu[i], decode_factor(cu[i]), &u);
+            const uint32_t both = qg[i] | qu[i] << 8;
+            float gu[2], dg, du, y;
+            decode<2>(&both, 1.0f, gu);
+            const float g = __fmul_rn(gu[0], decode_factor(cg[i])), u = __fmul_rn(gu[1], decode_factor(cu[i]));
             bwd_values<E, 1, MODE, E::kDeepScale>(&d[i], &g, &u, wr, acc, &dg, &du, &y);
             uint32_t o = 0u;
             E::put(&o, 0, dg);
@@ -408,34 +450,73 @@ __global__ void __launch_bounds__(T) ckpt8_bwd_narrow_kernel(const BwdParams p) 
         bwd_elements<E, K, swiglu::kPlain>(p, segment_at<K>(seg, p.row_packs, p.div), 1.0f, acc);
 }
 
-// With weights: a CTA takes a row, so dw[r] is a sum inside the CTA in a fixed
-// order.
-template <typename E, int VEC, int T>
-__global__ void __launch_bounds__(T) ckpt8_bwd_weighted_kernel(const BwdParams p) {
+// With weights a row's dw is one sum, in an order that the sizes fix.  ROWS = 4:
+// a warp takes a row (rows of few packs; T = 128).  ROWS = 1: a CTA does, or a
+// cluster of them when there are too few rows for the SMs; each CTA then leaves
+// its sum in shared memory and the first one adds them in rank order.
+//
+// Times (bf16, with y where it says so, of the 6680 GB/s copy): [8192, 2 x 4096]
+// 44.7 us 0.91, with y 52.5 us 0.96; [8192, 2 x 14336] 143 us 0.99.  Registers held
+// to 8 CTAs of 128 threads for 32-byte packs (45.9 us unbound, 62.9 us at 10).
+template <typename E, int VEC, int T, int ROWS>
+__global__ void __launch_bounds__(T, E::kBytes * VEC == 32 && T == 128 ? 8 : 1) ckpt8_bwd_weighted_kernel(const BwdParams p) {
     swiglu::await_previous_grid();
     swiglu::allow_next_grid();
-    __shared__ float red[T / 32];
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    static_assert(ROWS == 1 || ROWS == T / 32, "a row per CTA or per warp");
+    __shared__ float red[T / 32 + 1];
+    uint32_t rank, size;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t threads = ROWS == 1 ? (int32_t)size * T : 32;  // of a row
+    const int32_t id = ROWS == 1 ? (int32_t)rank * T + (int32_t)threadIdx.x : lane;
+    const int64_t rows_at_once = (int64_t)(gridDim.x / size) * ROWS;
+    for (int64_t r = (int64_t)(blockIdx.x / size) * ROWS + (ROWS == 1 ? 0 : warp); r < p.rows; r += rows_at_once) {
         const float wr = __ldg(p.w + r);
         float acc = 0.0f;
         if constexpr (VEC == 1) {
             constexpr int K = 4;
-            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-            for (int64_t c = warp * (32 * K); c < p.n; c += T * K)
+            for (int64_t c = (int64_t)(id >> 5) * (32 * K); c < p.n; c += (int64_t)threads * K)
                 bwd_elements<E, K, swiglu::kWeight>(p, {r, c + lane}, wr, acc);
         } else {
-            for (int32_t c = threadIdx.x; c < p.row_packs; c += T) bwd_one<E, VEC, swiglu::kWeight>(p, r, c, wr, acc);
+            // (two packs in flight held 96 registers and were 5-13 % slower in bf16)
+            for (int32_t c = id; c < p.row_packs; c += threads) {
+                BwdPack<E, VEC> pack;
+                pack.load(p, r, c);
+                pack.template finish<swiglu::kWeight>(p, r, c, wr, acc);
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
-        __syncthreads();  // red may still be read for the previous row
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
-        __syncthreads();
-        if (threadIdx.x == 0) {
+        if constexpr (ROWS > 1) {
+            if (lane == 0) p.dw[r] = acc;
+        } else {
+            __syncthreads();  // red may still be read for the previous row
+            if (lane == 0) red[warp] = acc;
+            __syncthreads();
             float t = 0.0f;
+            if (threadIdx.x == 0) {
 #pragma unroll
-            for (int k = 0; k < T / 32; ++k) t = __fadd_rn(t, red[k]);
-            p.dw[r] = t;
+                for (int k = 0; k < T / 32; ++k) t = __fadd_rn(t, red[k]);
+            }
+            if (size > 1) {
+                if (threadIdx.x == 0) red[T / 32] = t;
+                asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+                if (rank == 0 && threadIdx.x == 0) {
+                    const uint32_t own = (uint32_t)__cvta_generic_to_shared(red + T / 32);
+                    t = 0.0f;
+                    for (uint32_t k = 0; k < size; ++k) {
+                        uint32_t at;
+                        float v;
+                        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(own), "r"(k));
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+                        t = __fadd_rn(t, v);
+                    }
+                }
+                // no CTA goes on to its next row, or leaves, before its sum is read
+                asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+            }
+            if (rank == 0 && threadIdx.x == 0) p.dw[r] = t;
         }
     }
 }
