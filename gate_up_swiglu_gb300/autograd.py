@@ -154,6 +154,12 @@ class WeightedGateUpSwiGLUFunction(torch.autograd.Function):
         return dx, dbias, dw.reshape(ctx.w_shape).to(ctx.w_dtype), None
 
 
+def _ckpt8(x: torch.Tensor, weights: Optional[torch.Tensor]) -> torch.Tensor:
+    from .experts import Ckpt8SwiGLUFunction
+
+    return Ckpt8SwiGLUFunction.apply(x, weights)
+
+
 def bias_gate_up_swiglu(x: torch.Tensor, bias: torch.Tensor, in_place: bool = False) -> torch.Tensor:
     return BiasGateUpSwiGLUFunction.apply(x, bias, in_place)
 
@@ -173,21 +179,26 @@ class GateUpSwiGLU(torch.nn.Module):
     ``fallback_impl`` (logged once per reason); with ``fallback_impl=None`` it
     raises ``NotImplementedError``.  A bias is delegated the same way, as the
     page's module does, unless ``native_bias=True``: then the fused bias
-    kernels take it (BiasGateUpSwiGLUFunction).
+    kernels take it (BiasGateUpSwiGLUFunction).  With ``native_fp8=True``
+    fp8_input_store (without a bias) keeps the input as the 8-bit checkpoint
+    of swiglu_moe.h (Ckpt8SwiGLUFunction); nothing is kept in 16 bits then, so
+    ``in_place`` has no buffer to write over and does not apply.
     """
 
     def __init__(self, in_place: bool = False,
-                 fallback_impl: Optional[Callable] = None, native_bias: bool = False):
+                 fallback_impl: Optional[Callable] = None, native_bias: bool = False,
+                 native_fp8: bool = False):
         super().__init__()
         self.in_place = in_place
         self.fallback_impl = fallback_impl
         self.native_bias = native_bias
+        self.native_fp8 = native_fp8
         self._logged = set()
 
     def _unsupported(self, bias, fp8_input_store, cpu_offload_input) -> Optional[str]:
         if bias is not None and not self.native_bias:
             return "bias is not None"
-        if fp8_input_store:
+        if fp8_input_store and not (self.native_fp8 and bias is None):
             return "fp8_input_store=True"
         if cpu_offload_input:
             return "cpu_offload_input=True"
@@ -214,6 +225,8 @@ class GateUpSwiGLU(torch.nn.Module):
                              "(float32 or bfloat16)")
         if bias is not None:
             return BiasGateUpSwiGLUFunction.apply(intermediate, bias, self.in_place)
+        if fp8_input_store:
+            return _ckpt8(intermediate, None)
         return GateUpSwiGLUFunction.apply(intermediate, self.in_place)
 
 
@@ -221,17 +234,21 @@ class WeightedGateUpSwiGLU(torch.nn.Module):
     """Drop-in for Megatron's ``weighted_bias_swiglu_impl(input, bias, weights,
     fp8_input_store)`` of MoE routed experts: y = weights[token] * swiglu, the
     bias optional.  fp8 input storage goes to ``fallback_impl`` (logged once),
-    or raises ``NotImplementedError`` without one."""
+    or raises ``NotImplementedError`` without one; with ``native_fp8=True`` (and
+    no bias) it is the 8-bit checkpoint, as for GateUpSwiGLU."""
 
-    def __init__(self, in_place: bool = False, fallback_impl: Optional[Callable] = None):
+    def __init__(self, in_place: bool = False, fallback_impl: Optional[Callable] = None,
+                 native_fp8: bool = False):
         super().__init__()
         self.in_place = in_place
         self.fallback_impl = fallback_impl
+        self.native_fp8 = native_fp8
         self._logged = False
 
     def forward(self, intermediate: torch.Tensor, bias: Optional[torch.Tensor],
                 weights: torch.Tensor, fp8_input_store: bool = False) -> torch.Tensor:
-        if fp8_input_store:
+        native = fp8_input_store and self.native_fp8 and bias is None
+        if fp8_input_store and not native:
             if self.fallback_impl is None:
                 raise NotImplementedError("WeightedGateUpSwiGLU: fp8_input_store=True is not "
                                           "supported by the fused kernels and no fallback_impl "
@@ -247,6 +264,12 @@ class WeightedGateUpSwiGLU(torch.nn.Module):
         if intermediate.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"WeightedGateUpSwiGLU: dtype {intermediate.dtype} is not supported "
                              "(float32 or bfloat16)")
+        if native:
+            rows = math.prod(intermediate.shape[:-1])
+            if weights.numel() != rows:
+                raise ValueError(f"weights must hold one value per row ({rows}), got shape "
+                                 f"{tuple(weights.shape)}")
+            return _ckpt8(intermediate, weights)
         return WeightedGateUpSwiGLUFunction.apply(intermediate, bias, weights, self.in_place)
 
 

@@ -374,21 +374,39 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-inline std::atomic<EncodeTiled> g_encode{nullptr};
+using CtxGetCurrent = CUresult (*)(CUcontext *);
 
-// cuTensorMapEncodeTiled, looked up once.
-inline cudaError_t encoder(EncodeTiled &fn) {
-    fn = g_encode.load();
+inline std::atomic<EncodeTiled> g_encode{nullptr};
+inline std::atomic<CtxGetCurrent> g_ctx_current{nullptr};
+
+template <typename F>
+cudaError_t driver_entry(const char *name, std::atomic<F> &cache, F &fn) {
+    fn = cache.load();
     if (fn != nullptr) return cudaSuccess;
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                                     cudaEnableDefault, &q);
+    cudaError_t e = cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q);
     if (e != cudaSuccess) return e;
     if (q != cudaDriverEntryPointSuccess || p == nullptr) return cudaErrorNotSupported;
-    fn = reinterpret_cast<EncodeTiled>(p);
-    g_encode.store(fn);
+    fn = reinterpret_cast<F>(p);
+    cache.store(fn);
     return cudaSuccess;
+}
+
+// cuTensorMapEncodeTiled, looked up once.  It needs a current context, which a
+// thread that has made no runtime call yet (an autograd thread whose first work is
+// this) does not have: then the device's own is made current, as the runtime's
+// launch would do.
+inline cudaError_t encoder(EncodeTiled &fn) {
+    CtxGetCurrent current;
+    cudaError_t e = driver_entry("cuTensorMapEncodeTiled", g_encode, fn);
+    if (e == cudaSuccess) e = driver_entry("cuCtxGetCurrent", g_ctx_current, current);
+    if (e != cudaSuccess) return e;
+    CUcontext ctx = nullptr;
+    if (current(&ctx) == CUDA_SUCCESS && ctx != nullptr) return cudaSuccess;
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    return cudaSetDevice(dev);
 }
 
 }  // namespace tc

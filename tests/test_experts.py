@@ -1,0 +1,52 @@
+"""Policy of the experts' layer and of the opt-in fp8 input storage that needs no GPU."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def mods():
+    from conftest import build_library
+
+    build_library()
+    from gate_up_swiglu_gb300 import autograd, experts
+
+    return autograd, experts
+
+
+def test_experts_refusals(mods):
+    _, ex = mods
+    with pytest.raises(ValueError, match="checkpoint"):
+        ex.ExpertsSwiGLU(2, 16, 8, checkpoint="int4")
+    m = ex.ExpertsSwiGLU(2, 16, 8)
+    with pytest.raises(ValueError, match="counts"):
+        m(torch.zeros(4, 16).bfloat16(), torch.tensor([1, 2, 1]))
+    with pytest.raises(ValueError, match="rows"):
+        m(torch.zeros(2, 2, 16).bfloat16(), torch.tensor([1, 3]))
+    with pytest.raises(ValueError, match="CUDA"):
+        m(torch.zeros(4, 16).bfloat16(), torch.tensor([1, 3]))
+    with pytest.raises(ValueError, match="checkpoint"):
+        ex.ExpertsSwiGLUFunction.apply(torch.zeros(4, 16), None, m.w1, m.w2, torch.zeros(2), "int4")
+
+
+def test_group_ends(mods):
+    _, ex = mods
+    ends = ex.group_ends(torch.tensor([3, 0, 5]))
+    assert ends.dtype == torch.int32 and ends.tolist() == [3, 3, 8]
+
+
+def test_native_fp8_takes_the_input_without_a_bias_only(mods):
+    ag, _ = mods
+    m = ag.GateUpSwiGLU(native_fp8=True, native_bias=True)
+    with pytest.raises(ValueError, match="CUDA"):  # on its way to the kernels
+        m(torch.zeros(4, 8), None, True)
+    with pytest.raises(NotImplementedError, match="fp8_input_store"):
+        m(torch.zeros(4, 8), torch.zeros(8), True)
+    with pytest.raises(NotImplementedError, match="cpu_offload_input"):
+        m(torch.zeros(4, 8), None, True, True)
+    w = ag.WeightedGateUpSwiGLU(native_fp8=True)
+    with pytest.raises(NotImplementedError, match="fp8_input_store"):
+        w(torch.zeros(4, 8), torch.zeros(8), torch.ones(4), True)
+    with pytest.raises(ValueError, match="one value per row"):
+        w(torch.zeros(4, 8), None, torch.ones(3), True)
+    with pytest.raises(ValueError, match="CUDA"):
+        w(torch.zeros(4, 8), None, torch.ones(4), True)

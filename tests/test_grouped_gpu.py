@@ -277,6 +277,38 @@ def test_graph_replays_with_other_groups(sw):
             assert _same_bits(a + 0.0, b.bfloat16() + 0.0)
 
 
+def test_first_call_of_a_thread(sw):
+    """A thread that has made no CUDA call yet (as the autograd engine's) gives the
+    same bits; also for the dense first product, which encodes its maps likewise."""
+    import threading
+
+    g = _gen(10)
+    x, w, dy = _normal(g, 70, 72), _normal(g, 2, 128, 72), _normal(g, 70, 128)
+    ends = _ends([40, 30])
+
+    def calls():
+        return (sw.swiglu_grouped_mm_dgrad(dy, w, ends), sw.swiglu_grouped_mm_wgrad(dy, x, ends),
+                sw.swiglu_grouped_fc1_fwd(x, w, ends), sw.swiglu_fc1_fwd(x, w[0]))
+
+    want = calls()
+    torch.cuda.synchronize()
+    for first in range(4):
+        got = []
+
+        def work():
+            one = (lambda: sw.swiglu_grouped_mm_dgrad(dy, w, ends), lambda: sw.swiglu_grouped_mm_wgrad(dy, x, ends),
+                   lambda: sw.swiglu_grouped_fc1_fwd(x, w, ends), lambda: sw.swiglu_fc1_fwd(x, w[0]))[first]
+            got.append(one())
+            got.append(calls())
+            torch.cuda.synchronize()
+
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        assert len(got) == 2 and torch.equal(got[0], want[first])
+        assert all(torch.equal(a, b) for a, b in zip(got[1], want))
+
+
 def test_many_groups(sw):
     """1024 groups (the most of one call), most of them empty."""
     g = _gen(8)
