@@ -52,7 +52,10 @@ def _declare() -> None:
 _declare()
 
 
-_current_device = torch.cuda.current_device
+# the current device without the check that CUDA is initialised (these calls
+# have CUDA tensors in hand)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _ptr(t):
@@ -92,7 +95,7 @@ def _given(t: torch.Tensor, rows: int, cols: int, dtype, device, name: str) -> i
 
 def _weights(w: torch.Tensor, rows: int, device, name: str) -> int:
     """The address of an fp32 vector with one value per row."""
-    if w.dtype != torch.float32 or w.numel() != rows or not w.is_contiguous():
+    if w.dtype is not _F32 or w.numel() != rows or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {torch.float32} tensor of {rows} elements")
     if w.device != device:
         raise ValueError("all tensors must be on the same CUDA device")
@@ -183,26 +186,32 @@ def swiglu_ckpt8_bwd(dy: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, w:
     return dx, dw, y
 
 
-def _rows_and_experts(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, name: str):
-    """Checks shared by the products of rows x [rows, *] with w [E, N, K]."""
-    if not (x.is_cuda and w.is_cuda):
+def _check_products(a: torch.Tensor, b: torch.Tensor, ends: torch.Tensor) -> None:
+    """Checks shared by the products: two contiguous bf16 tensors on one CUDA device."""
+    device = a.get_device()
+    if device < 0 or b.get_device() < 0:
         raise ValueError("libswiglu operates on CUDA tensors only")
-    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+    if a.dtype is not _BF16 or b.dtype is not _BF16:
         raise ValueError("the grouped products take bfloat16 tensors")
-    if x.dim() != 2 or w.dim() != 3:
-        raise ValueError(f"{name} must have two dimensions and w three: [experts, N, K]")
-    if w.device != x.device:
+    if b.get_device() != device or ends.get_device() != device:
         raise ValueError("all tensors must be on the same CUDA device")
-    if not (x.is_contiguous() and w.is_contiguous()):
+    if not (a.is_contiguous() and b.is_contiguous()):
         raise ValueError("the grouped products need contiguous tensors")
-    _check_ends(ends, x, w.shape[0])
 
 
-def _check_ends(ends: torch.Tensor, x: torch.Tensor, groups: int) -> None:
-    if ends.dtype != torch.int32 or ends.numel() != groups or not ends.is_contiguous():
+def _rows_and_experts(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, name: str):
+    """The shapes of rows x [rows, *] and w [E, N, K]."""
+    _check_products(x, w, ends)
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != 3:
+        raise ValueError(f"{name} must have two dimensions and w three: [experts, N, K]")
+    _check_ends(ends, ws[0])
+    return xs, ws
+
+
+def _check_ends(ends: torch.Tensor, groups: int) -> None:
+    if ends.dtype is not _I32 or ends.numel() != groups or not ends.is_contiguous():
         raise ValueError(f"ends must be a contiguous {torch.int32} tensor of {groups} elements")
-    if ends.device != x.device:
-        raise ValueError("all tensors must be on the same CUDA device")
 
 
 def _result(t, shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
@@ -225,8 +234,7 @@ def swiglu_grouped_fc1_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
     8-bit checkpoint."""
     if save not in (None, "bf16", "fp8"):
         raise ValueError('save must be None, "bf16" or "fp8"')
-    _rows_and_experts(x, w, ends, "x")
-    (rows, K), (E, two_n, wk) = x.shape, w.shape
+    (rows, K), (E, two_n, wk) = _rows_and_experts(x, w, ends, "x")
     if wk != K or two_n % 2:
         raise ValueError("w must be [experts, 2n, K] with x's K")
     n = two_n // 2
@@ -244,8 +252,7 @@ def swiglu_grouped_fc1_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
 def swiglu_grouped_mm_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, y: torch.Tensor = None,
                           stream=None) -> torch.Tensor:
     """y[t] = W[e] x[t]: x [rows, K], w [E, N, K] -> y [rows, N]."""
-    _rows_and_experts(x, w, ends, "x")
-    (rows, K), (E, N, wk) = x.shape, w.shape
+    (rows, K), (E, N, wk) = _rows_and_experts(x, w, ends, "x")
     if wk != K:
         raise ValueError("w must be [experts, N, K] with x's K")
     y = _result(y, (rows, N), x.dtype, x, "y")
@@ -257,8 +264,7 @@ def swiglu_grouped_mm_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, 
 def swiglu_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, dx: torch.Tensor = None,
                             stream=None) -> torch.Tensor:
     """dx[t] = W[e]^T dy[t]: dy [rows, N], w [E, N, K] -> dx [rows, K]."""
-    _rows_and_experts(dy, w, ends, "dy")
-    (rows, N), (E, wn, K) = dy.shape, w.shape
+    (rows, N), (E, wn, K) = _rows_and_experts(dy, w, ends, "dy")
     if wn != N:
         raise ValueError("w must be [experts, N, K] with dy's N")
     dx = _result(dx, (rows, K), dy.dtype, dy, "dx")
@@ -272,14 +278,9 @@ def swiglu_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, ends: torch.Tenso
     """dW[e] = sum over the group's rows of dy[t]^T x[t]: dy [rows, N], x [rows, K]
     -> dw [E, N, K] of ``dtype`` (bfloat16, the default, or float32; that of ``dw``
     when one is given).  ``accumulate`` adds to a float32 ``dw``."""
-    if not (dy.is_cuda and x.is_cuda):
-        raise ValueError("libswiglu operates on CUDA tensors only")
-    if dy.dtype != torch.bfloat16 or x.dtype != torch.bfloat16:
-        raise ValueError("the grouped products take bfloat16 tensors")
-    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or dy.device != x.device:
-        raise ValueError("dy must be [rows, N] and x [rows, K] over the same rows, on one device")
-    if not (dy.is_contiguous() and x.is_contiguous()):
-        raise ValueError("the grouped products need contiguous tensors")
+    _check_products(dy, x, ends)
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy must be [rows, N] and x [rows, K] over the same rows")
     if dtype is None:
         dtype = dw.dtype if dw is not None else torch.bfloat16
     if dtype not in _DTYPE:
@@ -287,7 +288,7 @@ def swiglu_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, ends: torch.Tenso
     if accumulate and (dw is None or dtype != torch.float32):
         raise ValueError("accumulate adds to a float32 dw: give one")
     (rows, N), K, E = dy.shape, x.shape[1], ends.numel()
-    _check_ends(ends, dy, E)
+    _check_ends(ends, E)
     dw = _result(dw, (E, N, K), dtype, dy, "dw")
     _call("swiglu_grouped_mm_wgrad", lib.swiglu_grouped_mm_wgrad, dy, stream, dy.data_ptr(), x.data_ptr(),
           ends.data_ptr(), dw.data_ptr(), rows, E, N, K, SWIGLU_BF16, _DTYPE[dtype], 1 if accumulate else 0)
