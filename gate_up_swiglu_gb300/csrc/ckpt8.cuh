@@ -52,17 +52,14 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
 // N values (N = 1 or a multiple of 2) scaled by `f` to N codes.  The largest
 // values of fp32 would round up to 256 * 2^120 = 2^128, which fp32 cannot hold:
 // they keep the code of 240.  One test of the largest value tells whether any
-// of this, or an infinity, has to be looked at.
-template <int N>
-__device__ __forceinline__ void encode(const float *v, float f, uint32_t *out) {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
-    const bool rare = m > 2.97747071e38f;  // 1.75 * 2^127
+// of this, or an infinity, has to be looked at; kCare: it has.
+template <int N, bool kCare>
+__device__ __forceinline__ void encode_values(const float *v, float f, uint32_t *out) {
     const float top = f == 7.52316384526264e-37f ? 240.0f : 448.0f;  // 2^-120: the largest scale
     const auto one = [&](int i) {
         float t = __fmul_rn(v[i], f);
-        if (rare) t = fabsf(v[i]) == INFINITY ? __uint_as_float(0x7fc00000u) : t > top ? top : t < -top ? -top : t;
+        if (kCare)
+            t = fabsf(v[i]) == INFINITY ? __uint_as_float(0x7fc00000u) : t > top ? top : t < -top ? -top : t;
         return t;
     };
     if (N == 1) {
@@ -77,6 +74,17 @@ __device__ __forceinline__ void encode(const float *v, float f, uint32_t *out) {
                 out[i / 4] |= h << 16;
         }
     }
+}
+
+template <int N>
+__device__ __forceinline__ void encode(const float *v, float f, uint32_t *out) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
+    if (m <= 2.97747071e38f)  // 1.75 * 2^127
+        encode_values<N, false>(v, f, out);
+    else
+        encode_values<N, true>(v, f, out);
 }
 
 // N codes to the values they stand for (e4m3 is exact in fp16 and fp32).
