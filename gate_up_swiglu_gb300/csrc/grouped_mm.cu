@@ -81,11 +81,11 @@ constexpr int OFF_ABORT = OFF_TMEM + 4;
 constexpr int STATE_BYTES = 512;
 static_assert(OFF_ABORT + 4 <= STATE_BYTES, "barriers and state fit their region");
 // the epilogue's staging, per warp: 32 rows of 64 bytes for bulk stores (64-byte
-// swizzle); kFc1: 32 rows of 32 gates and 32 ups per pair of warps, fp32, rows
+// swizzle); kFc1: 16 rows of 32 gates and 32 ups per pair of warps, fp32, rows
 // padded by 4 words
 constexpr int STG_WARP_BYTES = 32 * 64;
 constexpr int STG_ROW_FC1 = 68;
-constexpr int STG_PAIR_FC1 = 32 * STG_ROW_FC1 * 4;
+constexpr int STG_PAIR_FC1 = 16 * STG_ROW_FC1 * 4;
 constexpr int STG_BYTES = 18 * 1024;
 constexpr int TABLE_BYTES = 2 * (kMaxGroups + 2) * 4;
 constexpr int SMEM_BYTES = RING_BYTES + STG_BYTES + STATE_BYTES + (TABLE_BYTES + 15) / 16 * 16 + 1024;
@@ -243,39 +243,38 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Groups &g, int t)
 
 __device__ __forceinline__ float4 lds128(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// 16 bf16 at p, of which the first `live` (a multiple of 8) are stored.
-__device__ __forceinline__ void store_bf16x16(__nv_bfloat16 *p, const uint32_t (&w)[8], int live, bool wide) {
-    if (wide) {
-        if (live > 0) store32(p, w);
-    } else {
-        if (live > 0) store16(p, w[0], w[1], w[2], w[3]);
-        if (live > 8) store16(p + 8, w[4], w[5], w[6], w[7]);
-    }
-}
-
-__device__ __forceinline__ void store_codes16(uint8_t *p, const uint32_t (&w)[4], int live, bool wide) {
-    if (wide) {
-        if (live > 0) store16(p, w[0], w[1], w[2], w[3]);
-    } else {
-        if (live > 0) swiglu::St<8, swiglu::kStStream>::run(p, w);
-        if (live > 8) swiglu::St<8, swiglu::kStStream>::run(p + 8, w + 2);
-    }
-}
-
-// y for 16 gates and ups of one row, from fp32, rounded once: the operations of
-// the streaming kernels (swiglu::activation), with the row weight last.
-template <bool kMayDeep>
-__device__ __forceinline__ void activate16(const float (&g)[16], const float (&u)[16], float w, uint32_t (&out)[8]) {
+// y for 8 gates and ups of one row, from fp32, rounded once: the operations of
+// the streaming kernels (swiglu::activation), with the row weight last.  Without a
+// gate below -64 two elements go through each multiplication and addition (each
+// lane rounded as the scalar operation rounds).
+__device__ __forceinline__ void activate8(const float (&g)[8], const float (&u)[8], float w, uint32_t (&out)[4]) {
+    float gmin = g[0];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        float r[2];
+    for (int i = 1; i < 8; ++i) gmin = fminf(gmin, g[i]);
+    if (gmin < -64.0f) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const swiglu::Act act = swiglu::activation<swiglu::BF16, false, kMayDeep>(g[i + h]);
-            r[h] = __fmul_rn(__fmul_rn(act.silu, u[i + h]), w);
-            if (kMayDeep) r[h] = __fmul_rn(r[h], act.scale);
+        for (int i = 0; i < 8; i += 2) {
+            float r[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const swiglu::Act act = swiglu::activation<swiglu::BF16, false, true>(g[i + h]);
+                r[h] = __fmul_rn(__fmul_rn(__fmul_rn(act.silu, u[i + h]), w), act.scale);
+            }
+            swiglu::BF16::put2(out, i, r[0], r[1]);
         }
-        swiglu::BF16::put2(out, i, r[0], r[1]);
+    } else {
+        using namespace swiglu;
+        const uint64_t neg_log2e = x2(-kLog2e, -kLog2e), one = x2(1.0f, 1.0f), w2 = x2(w, w);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const uint64_t g2 = x2(g[i], g[i + 1]), u2 = x2(u[i], u[i + 1]);
+            float t0, t1, d0, d1, r0, r1;
+            x2_split(mul_x2(g2, neg_log2e), t0, t1);
+            x2_split(add_x2(one, x2(ex2_approx(t0), ex2_approx(t1))), d0, d1);
+            const uint64_t s2 = x2(rcp_approx(d0), rcp_approx(d1));
+            x2_split(mul_x2(mul_x2(mul_x2(g2, s2), u2), w2), r0, r1);
+            BF16::put2(out, i, r0, r1);
+        }
     }
 }
 
@@ -304,15 +303,14 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int m, int 
 }
 
 // Warps: 0 loads, 1 MMA, 2 .. epilogue, then the scheduler and (kWgrad) the warp
-// that zeroes rows.  The epilogue has four warps, one per quarter of the
-// accumulator's lanes, or eight, which take every other 32 columns each.
+// that zeroes rows.  The epilogue has two warps per quarter of the accumulator's
+// lanes, which take every other chunk of columns each (with one the tile of a
+// short contraction took 4.3 instead of 3.7 us, kFc1 5.6 instead of 4.9).
+constexpr int kEpi = 8;
+constexpr int kScheduler = 2 + kEpi;
 template <int MODE>
-constexpr int kEpiWarps = MODE == kFc1 ? 4 : 8;
-template <int MODE>
-constexpr int kScheduler = 2 + kEpiWarps<MODE>;
-template <int MODE>
-constexpr int kPairThreads = 32 * (3 + kEpiWarps<MODE> + (MODE == kWgrad ? 1 : 0));
-static_assert(8 * STG_WARP_BYTES <= STG_BYTES && 2 * STG_PAIR_FC1 <= STG_BYTES, "the epilogue's staging");
+constexpr int kPairThreads = 32 * (3 + kEpi + (MODE == kWgrad ? 1 : 0));
+static_assert(kEpi * STG_WARP_BYTES <= STG_BYTES && kEpi / 2 * STG_PAIR_FC1 <= STG_BYTES, "the epilogue's staging");
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 1)
@@ -339,7 +337,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
     constexpr bool kBMn = MODE == kWgrad;
     // readers of a tile: the MMA thread and, of both CTAs, the producer, the
     // epilogue warps and, for the weight gradient, the warp that zeroes rows
-    constexpr int kEpi = kEpiWarps<MODE>;
     constexpr int kReaders = 1 + 2 * (1 + kEpi + (MODE == kWgrad ? 1 : 0));
 
     const uint32_t rank = cluster_rank();
@@ -418,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
         return t;
     };
 
-    if (warp == kScheduler<MODE>) {
+    if (warp == kScheduler) {
         // ---- scheduler (the leader's): finds each tile's group and publishes it to
         // both CTAs while the one before is worked on.  The next tile is that of a
         // cluster whose launch it cancels, asked for once there is room for it: pairs
@@ -577,16 +574,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
         // ---- epilogue (both CTAs): this CTA's 128 lanes of the accumulator,
         // a quarter per warp
         const int quarter = warp & 3, set = (warp - 2) >> 2;
-        constexpr int kStep = 8 * kEpi;  // columns from one chunk of a warp to its next
+        constexpr int kChunk = MODE == kFc1 ? 16 : 32;  // columns of a warp at a time, and
+        constexpr int kStep = kChunk * kEpi / 4;        // from one chunk to its next
         const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
-        float *stg_pair = reinterpret_cast<float *>(staging + (quarter >> 1) * STG_PAIR_FC1);
+        float *stg_pair = reinterpret_cast<float *>(staging + (2 * set + (quarter >> 1)) * STG_PAIR_FC1);
         unsigned char *to = staging + (4 * set + quarter) * STG_WARP_BYTES;
         // the buffer, once the bulk store that read it last is done with it
         const auto free_buffer = [&]() {
             if (elect_one()) bulk_wait_read<0>();
             __syncwarp();
         };
-        const int bar_id = 1 + (quarter >> 1);
+        const int bar_id = 1 + 2 * set + (quarter >> 1);
         int lt = 0;
         bool ok = true;
         // the warp leaves the loop as one: the tile id, the abort flag and the
@@ -616,16 +614,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                 const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
                 // (reading the next 32 columns ahead of storing these was no faster:
                 // 4.7 us per 256 x 256 tile of one contraction block against 4.3)
-                if (32 * set >= width) {  // no columns for this warp
+                if (kChunk * set >= width) {  // no columns for this warp
                     if (lane == 0) mbar_arrive_cluster(acc_empty_leader0 + 8 * acc);
                     continue;
                 }
 #pragma unroll 1
-                for (int c = 32 * set; c < width; c += kStep) {
-                    uint32_t v[32];
+                for (int c = kChunk * set; c < width; c += kStep) {
+                    uint32_t v[kChunk];
                     if constexpr (MODE == kMm || MODE == kDgrad) {
                         tmem_load_16x32(tbase + c, v);  // lanes 0 - 15 and 16 - 31 of the quarter
                         tmem_load_16x32(tbase + (16u << 16) + c, v + 16);
+                    } else if constexpr (MODE == kFc1) {
+                        tmem_load16(tbase + c, v);
                     } else {
                         tmem_load32(tbase + c, v);
                     }
@@ -637,7 +637,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                     }
                     if (kblocks == 0) {  // nothing was accumulated
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                        for (int i = 0; i < kChunk; ++i) v[i] = 0u;
                     }
                     if constexpr (MODE == kFc1) {
                         const auto pair_sync = [&]() {
@@ -645,69 +645,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                         };
                         pair_sync();  // the previous chunk has been read
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 16; ++i)
                             stg_pair[i * STG_ROW_FC1 + 32 * (quarter & 1) + lane] = __uint_as_float(v[i]);
                         pair_sync();
-                        // two lanes per row, 16 features each
-                        const int tk = 16 * (quarter & 1) + (lane >> 1), h = lane & 1;
-                        const float *src = stg_pair + tk * STG_ROW_FC1 + 16 * h;
-                        float g[16], u[16];
+                        // four lanes per row, 8 features each
+                        const int tk = 8 * (quarter & 1) + (lane >> 2), part = lane & 3;
+                        const float *src = stg_pair + tk * STG_ROW_FC1 + 8 * part;
+                        float g[8], u[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             const float4 a = lds128(src + 4 * i), b = lds128(src + 32 + 4 * i);
                             g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
                             u[4 * i] = b.x, u[4 * i + 1] = b.y, u[4 * i + 2] = b.z, u[4 * i + 3] = b.w;
                         }
                         const int n = p.features;
-                        const int col = t.m0 + 64 * (int)rank + 32 * (quarter >> 1) + 16 * h;
-                        const bool in = c + tk < t.cnt;
-                        const int live = in ? n - col : 0;
+                        const int col = t.m0 + 64 * (int)rank + 32 * (quarter >> 1) + 8 * part;
+                        const bool in = c + tk < t.cnt && col < n;  // (n is a multiple of 8)
                         const int64_t row = (int64_t)t.r0 + t.n0 + c + tk;
                         if (p.q != nullptr) {
-                            // both lanes of the row hold half of its 32-column block
-                            float mg = ckpt8::finite_amax<16>(g), mu = ckpt8::finite_amax<16>(u);
-                            mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, 1));
-                            mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, 1));
+                            // the row's four lanes hold its 32-column block
+                            float mg = ckpt8::finite_amax<8>(g), mu = ckpt8::finite_amax<8>(u);
+#pragma unroll
+                            for (int o = 1; o < 4; o <<= 1) {
+                                mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+                                mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+                            }
                             const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
-                            uint32_t qg[4], qu[4];
-                            ckpt8::encode<16>(g, ckpt8::encode_factor(cg), qg);
-                            ckpt8::encode<16>(u, ckpt8::encode_factor(cu), qu);
-                            uint8_t *qr = p.q + row * 2 * n + col;
-                            store_codes16(qr, qg, live, n % 16 == 0);
-                            store_codes16(qr + n, qu, live, n % 16 == 0);
-                            if (live > 0 && h == 0) {
-                                const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
-                                uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
-                                sr[0] = (uint8_t)cg;
-                                sr[nb] = (uint8_t)cu;
+                            if (in) {
+                                using St8 = swiglu::St<8, swiglu::kStStream>;
+                                uint32_t q[2];
+                                uint8_t *qr = p.q + row * 2 * n + col;
+                                ckpt8::encode<8>(g, ckpt8::encode_factor(cg), q);
+                                St8::run(qr, q);
+                                ckpt8::encode<8>(u, ckpt8::encode_factor(cu), q);
+                                St8::run(qr + n, q);
+                                if (part == 0) {
+                                    const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
+                                    uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
+                                    sr[0] = (uint8_t)cg;
+                                    sr[nb] = (uint8_t)cu;
+                                }
                             }
                         }
-                        if (live > 0) {
-                            const bool wide = n % 16 == 0;
+                        if (in) {
+                            uint32_t o[4];
                             if (p.fc1 != nullptr) {
-                                uint32_t pg[8], pu[8];
-#pragma unroll
-                                for (int i = 0; i < 16; i += 2) {
-                                    swiglu::BF16::put2(pg, i, g[i], g[i + 1]);
-                                    swiglu::BF16::put2(pu, i, u[i], u[i + 1]);
-                                }
                                 __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
-                                const bool fw = wide && reinterpret_cast<uintptr_t>(p.fc1) % 32 == 0;
-                                store_bf16x16(fr, pg, live, fw);
-                                store_bf16x16(fr + n, pu, live, fw);
+                                swiglu::store_pack<swiglu::BF16, 8>(o, g);
+                                store16(fr, o[0], o[1], o[2], o[3]);
+                                swiglu::store_pack<swiglu::BF16, 8>(o, u);
+                                store16(fr + n, o[0], o[1], o[2], o[3]);
                             }
-                            float w = 1.0f;
-                            if (p.probs != nullptr && t.group != p.groups) w = p.probs[row];
-                            float gmin = g[0];
-#pragma unroll
-                            for (int i = 1; i < 16; ++i) gmin = fminf(gmin, g[i]);
-                            uint32_t o[8];
-                            if (gmin < -64.0f)
-                                activate16<true>(g, u, w, o);
-                            else
-                                activate16<false>(g, u, w, o);
-                            store_bf16x16(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, o, live,
-                                          wide && reinterpret_cast<uintptr_t>(p.out) % 32 == 0);
+                            const float w = p.probs != nullptr && t.group != p.groups ? p.probs[row] : 1.0f;
+                            activate8(g, u, w, o);
+                            store16(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, o[0], o[1], o[2], o[3]);
                         }
                     } else if constexpr (MODE == kWgrad) {
                         // a lane is a row of dW; stores beyond its rows and columns
@@ -799,7 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
             } while (kb < kblocks);
         }
         if (elect_one()) bulk_wait<0>();  // the stores, before their shared memory goes
-    } else if (MODE == kWgrad && warp == kScheduler<MODE> + 1) {
+    } else if (MODE == kWgrad && warp == kScheduler + 1) {
         // ---- zero the rows beyond the group in its last stage (both CTAs)
         int it = 0;
         uint32_t uses = 0;  // phase of each stage's tail barrier
