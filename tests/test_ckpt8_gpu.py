@@ -278,3 +278,23 @@ def test_large_offsets(sw):
     assert_parity(y2[pick.cuda()], ry.bfloat16(), "y")
     tol = (n / 32 + 16) * 2.0 ** -24 * rabs + 2.0 ** -23 * rdw.abs() + 2.0 ** -17 * rabs
     assert bool(((dw[pick.cuda()].cpu().double() - rdw).abs() <= tol).all())
+
+
+def test_python_layer_refusals(sw):
+    x = torch.zeros(4, 64, device="cuda")
+    y, q, s = sw.swiglu_ckpt8_fwd(x)
+    w = torch.ones(4, device="cuda")
+    dy = torch.zeros(4, 32, device="cuda")
+    for bad in (lambda: sw.swiglu_ckpt8_fwd(x.half()), lambda: sw.swiglu_ckpt8_fwd(x, w[:3]),
+                lambda: sw.swiglu_ckpt8_fwd(x, w.double()), lambda: sw.swiglu_ckpt8_fwd(x, w.cpu()),
+                lambda: sw.swiglu_ckpt8_fwd(x[:, ::2]), lambda: sw.swiglu_ckpt8_fwd(x, None, y.bfloat16()),
+                lambda: sw.swiglu_ckpt8_fwd(x, None, y[:3]), lambda: sw.swiglu_ckpt8_fwd(x, None, None, q.view(torch.uint8)),
+                lambda: sw.swiglu_ckpt8_fwd(x, None, None, q, s[:, :1]), lambda: sw.swiglu_ckpt8_bwd(dy, q.view(torch.uint8), s),
+                lambda: sw.swiglu_ckpt8_bwd(dy, q[:3], s), lambda: sw.swiglu_ckpt8_bwd(dy, q, s[:, :1]),
+                lambda: sw.swiglu_ckpt8_bwd(dy[:, :31], q, s), lambda: sw.swiglu_ckpt8_bwd(dy, q, s, w[:2]),
+                lambda: sw.swiglu_ckpt8_bwd(dy, q, s, dw=w), lambda: sw.swiglu_ckpt8_bwd(dy, q.cpu(), s),
+                lambda: sw.swiglu_ckpt8_bwd(dy, q, s, w, y=dy.bfloat16())):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(sw.SwigluError, match="ALIAS"):
+        sw.swiglu_ckpt8_bwd(dy, q, s, y=dy)

@@ -309,6 +309,50 @@ def test_first_call_of_a_thread(sw):
         assert all(torch.equal(a, b) for a, b in zip(got[1], want))
 
 
+@pytest.mark.parametrize("counts,n", [([5, 3], 40), ([300, 270, 200, 130], 2056)])
+def test_deep_gates(sw, counts, n):
+    """Gates from -130 to 130 (integers, so the products are exact): y within one
+    bf16 step, subnormal results and zeros included, on both kernels."""
+    g = _gen(11)
+    rows, E, K = sum(counts), len(counts), 64
+    x = torch.zeros(rows, K, device="cuda")
+    x[:, 0] = torch.randint(-130, 131, (rows,), generator=g, device="cuda").float()
+    x[:, 1] = torch.randint(-8, 9, (rows,), generator=g, device="cuda").float()
+    w = torch.zeros(E, 2 * n, K, device="cuda")
+    w[:, :n, 0] = 1.0  # the gate is x[0]
+    w[:, n:, 1] = torch.randint(-3, 4, (E, n), generator=g, device="cuda").float()
+    x, w, ends = x.bfloat16(), w.bfloat16(), _ends(counts)
+    p = torch.rand(rows, generator=g, device="cuda")
+    ref = R.mm(x, w, ends)[0]
+    want = (R.silu64(ref[:, :n]) * ref[:, n:] * p.double()[:, None]).bfloat16()
+    y = sw.swiglu_grouped_fc1_fwd(x, w, ends, p)
+    assert int((bf16_ordered(y) - bf16_ordered(want)).abs().max()) <= 1
+
+
+def test_python_layer_refusals(sw):
+    g = _gen(12)
+    x, w, ends = _ints(g, 20, 16), _ints(g, 2, 32, 16), _ends([12, 8])
+    dy = _ints(g, 20, 32)
+    for bad in (lambda: sw.swiglu_grouped_mm_fwd(x.float(), w, ends), lambda: sw.swiglu_grouped_mm_fwd(x, w.float(), ends),
+                lambda: sw.swiglu_grouped_mm_fwd(x, w, ends.long()), lambda: sw.swiglu_grouped_mm_fwd(x, w, ends[:1]),
+                lambda: sw.swiglu_grouped_mm_fwd(x, w, ends.cpu()), lambda: sw.swiglu_grouped_mm_fwd(x.cpu(), w, ends),
+                lambda: sw.swiglu_grouped_mm_fwd(dy, w, ends), lambda: sw.swiglu_grouped_mm_fwd(x[:, ::2], w, ends),
+                lambda: sw.swiglu_grouped_mm_fwd(x, w.transpose(1, 2), ends), lambda: sw.swiglu_grouped_mm_fwd(x, w[0], ends),
+                lambda: sw.swiglu_grouped_mm_fwd(x, w, ends, y=dy[:, :16]), lambda: sw.swiglu_grouped_mm_dgrad(x, w, ends),
+                lambda: sw.swiglu_grouped_mm_wgrad(dy, x[:10], ends), lambda: sw.swiglu_grouped_mm_wgrad(dy, x, ends, accumulate=True),
+                lambda: sw.swiglu_grouped_mm_wgrad(dy, x, ends, dtype=torch.float16),
+                lambda: sw.swiglu_grouped_mm_wgrad(dy, x, ends, dw=w, accumulate=True),
+                lambda: sw.swiglu_grouped_fc1_fwd(x, w[:, :31], ends), lambda: sw.swiglu_grouped_fc1_fwd(x, w, ends, x[:, 0]),
+                lambda: sw.swiglu_grouped_fc1_fwd(x, w, ends, torch.rand(19, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(sw.SwigluError, match="SHAPE"):  # widths that are no multiple of 8
+        sw.swiglu_grouped_mm_fwd(_ints(g, 4, 12), _ints(g, 1, 8, 12), _ends([4]))
+    square = _ints(g, 20, 32)
+    with pytest.raises(sw.SwigluError, match="ALIAS"):
+        sw.swiglu_grouped_mm_fwd(square, _ints(g, 2, 32, 32), ends, y=square)
+
+
 def test_many_groups(sw):
     """1024 groups (the most of one call), most of them empty."""
     g = _gen(8)
