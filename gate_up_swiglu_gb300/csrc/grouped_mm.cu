@@ -136,17 +136,24 @@ struct Tile {
     int r0, rows;            // the group's rows
 };
 
-// Write a tile (group -1: none left) into the slot at `slot` of both CTAs and
-// release it with an arrive on each CTA's barrier; read one.
+// Write a tile (group -1: none left) into the slot at `slot` of both CTAs, counted
+// as bytes on each CTA's barrier `bar`; read one.
+constexpr uint32_t kTileBytes = 24;
+
 __device__ __forceinline__ void publish(uint32_t slot, uint32_t bar, const Tile &t) {
 #pragma unroll
     for (uint32_t r = 0; r < 2; ++r) {
-        const uint32_t to = map_to_rank(slot, r);
-        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(t.group), "r"(t.m0), "r"(t.n0),
-                     "r"(t.cnt)
+        const uint32_t to = map_to_rank(slot, r), on = map_to_rank(bar, r);
+        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(on),
+                     "r"(kTileBytes)
                      : "memory");
-        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to + 16), "r"(t.r0), "r"(t.rows) : "memory");
-        mbar_arrive_cluster(map_to_rank(bar, r));
+        asm volatile(
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(to),
+            "r"(on), "r"(t.group), "r"(t.m0), "r"(t.n0), "r"(t.cnt)
+            : "memory");
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%2, %3}, [%1];" ::"r"(to + 16),
+                     "r"(on), "r"(t.r0), "r"(t.rows)
+                     : "memory");
     }
 }
 
@@ -400,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
         Tile t;
         t.group = -1;
         if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1)) t = read_tile(tile0 + 32 * slot);
-        mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+        mbar_arrive_cluster_read(tile_empty_leader0 + 8 * slot);
         return t;
     };
     // the same for a whole warp
@@ -411,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
         Tile t = read_tile(tile0 + 32 * slot);
         if (!ok) t.group = -1;
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
+        if (lane == 0) mbar_arrive_cluster_read(tile_empty_leader0 + 8 * slot);
         return t;
     };
 
@@ -615,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                 // (reading the next 32 columns ahead of storing these was no faster:
                 // 4.7 us per 256 x 256 tile of one contraction block against 4.3)
                 if (kChunk * set >= width) {  // no columns for this warp
-                    if (lane == 0) mbar_arrive_cluster(acc_empty_leader0 + 8 * acc);
+                    if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
                     continue;
                 }
 #pragma unroll 1
@@ -633,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                     if (c + kStep >= width) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(acc_empty_leader0 + 8 * acc);
+                        if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
                     }
                     if (kblocks == 0) {  // nothing was accumulated
 #pragma unroll
@@ -1192,7 +1199,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
             }
         }
     }
-    if (size > 1) cluster_sync();  // no CTA leaves while another may still read its sums
+    __syncwarp();
+    if (size > 1) cluster_sync_read();  // no CTA leaves while another may still read its sums
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NT) : "memory");

@@ -248,6 +248,13 @@ __device__ __forceinline__ void cluster_sync() {
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The same where nothing written has to be seen afterwards (what was read from the
+// other CTAs has arrived): it does not wait for this CTA's stores.
+__device__ __forceinline__ void cluster_sync_read() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n"
+                 "barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // TMA load into this CTA's shared memory whose completion is counted on an
 // mbarrier that may live in the peer CTA (the leader's).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map,
@@ -334,6 +341,13 @@ __device__ __forceinline__ void mma_commit_local_pair(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
                  : "memory");
+}
+
+// The same where no write has to be seen in the other CTA (tensor memory or
+// shared memory has been read and may be written again): a release at cluster
+// scope waits some 700 ns for the thread's earlier writes.
+__device__ __forceinline__ void mbar_arrive_cluster_read(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 // Cluster launch control: ask to cancel the launch of a cluster of this grid
