@@ -30,10 +30,13 @@
 // drops it.
 //
 // The weight gradient's contraction runs over a group's rows, so its last block
-// of 64 would take in rows of the next group.  Those loads are counted on a
-// barrier of their own, the last warp of each CTA zeroes the rows beyond the group in
-// shared memory (a product with 0 would not do: a neighbour's row may hold
-// NaN), and only then the stage is handed to the tensor cores.
+// of 64 would take in rows of the next group (and a product with 0 would not do
+// for them: a neighbour's row may hold NaN).  The pair kernel puts that block
+// together from boxes of 1, 2, 4, ... 32 rows, and up to the next multiple of 16,
+// an instruction's depth, from boxes beyond the tensor's end, which are filled with
+// zeros: the tensor cores see nothing but what TMA wrote.  (Zeroing the rows from a
+// warp instead, handed on with a release to the other CTA, took 2000 cycles per
+// tile that the ring did not cover.)
 #include <climits>
 
 #include "ckpt8.cuh"
@@ -67,8 +70,7 @@ constexpr int kTileSlots = 2;
 // byte offsets in the region after the ring
 constexpr int OFF_FULL = 0;
 constexpr int OFF_EMPTY = OFF_FULL + 8 * STAGES;
-constexpr int OFF_TAIL = OFF_EMPTY + 8 * STAGES;          // this CTA's loads of a group's last rows (kWgrad)
-constexpr int OFF_ACC_FULL = OFF_TAIL + 8 * STAGES;
+constexpr int OFF_ACC_FULL = OFF_EMPTY + 8 * STAGES;
 constexpr int OFF_ACC_EMPTY = OFF_ACC_FULL + 16;
 constexpr int OFF_MMA_DONE = OFF_ACC_EMPTY + 16;
 constexpr int OFF_TILE_FULL = OFF_MMA_DONE + 8;
@@ -105,6 +107,7 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 struct Params {
     CUtensorMap a;     // the M side
     CUtensorMap b[4];  // the N side, boxes of 16, 32, 64 and 128 rows (kWgrad: b[0] alone, 64 rows)
+    CUtensorMap part_a[6], part_b[6];  // kWgrad, a group's last rows: boxes of 1, 2, ... 32 rows
     CUtensorMap c;     // the result (not kFc1), boxes of 64 bytes by 32 rows
     const int32_t *ends;
     const float *probs;      // kFc1
@@ -309,18 +312,16 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int m, int 
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// Warps: 0 loads, 1 MMA, 2 .. epilogue, then the scheduler and (kWgrad) the warp
-// that zeroes rows.  The epilogue has two warps per quarter of the accumulator's
+// Warps: 0 loads, 1 MMA, 2 .. epilogue, then the scheduler.  The epilogue has two warps per quarter of the accumulator's
 // lanes, which take every other chunk of columns each (with one the tile of a
 // short contraction took 4.3 instead of 3.7 us, kFc1 5.6 instead of 4.9).
 constexpr int kEpi = 8;
 constexpr int kScheduler = 2 + kEpi;
-template <int MODE>
-constexpr int kPairThreads = 32 * (3 + kEpi + (MODE == kWgrad ? 1 : 0));
+constexpr int kPairThreads = 32 * (3 + kEpi);
 static_assert(kEpi * STG_WARP_BYTES <= STG_BYTES && kEpi / 2 * STG_PAIR_FC1 <= STG_BYTES, "the epilogue's staging");
 
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     grouped_mm_kernel(const __grid_constant__ Params p) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -329,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
     unsigned char *staging = smem + RING_BYTES;
     unsigned char *state = staging + STG_BYTES;
     const uint32_t st0 = smem_addr(state);
-    const uint32_t full0 = st0 + OFF_FULL, empty0 = st0 + OFF_EMPTY, tail0 = st0 + OFF_TAIL;
+    const uint32_t full0 = st0 + OFF_FULL, empty0 = st0 + OFF_EMPTY;
     const uint32_t acc_full0 = st0 + OFF_ACC_FULL, acc_empty0 = st0 + OFF_ACC_EMPTY;
     const uint32_t mma_done = st0 + OFF_MMA_DONE;
     const uint32_t tile_full0 = st0 + OFF_TILE_FULL, tile_empty0 = st0 + OFF_TILE_EMPTY;
@@ -342,9 +343,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
 
     constexpr bool kAMn = MODE == kDgrad || MODE == kWgrad;
     constexpr bool kBMn = MODE == kWgrad;
-    // readers of a tile: the MMA thread and, of both CTAs, the producer, the
-    // epilogue warps and, for the weight gradient, the warp that zeroes rows
-    constexpr int kReaders = 1 + 2 * (1 + kEpi + (MODE == kWgrad ? 1 : 0));
+    // readers of a tile: the MMA thread and, of both CTAs, the producer and the
+    // epilogue warps
+    constexpr int kReaders = 1 + 2 * (1 + kEpi);
 
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
@@ -353,11 +354,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            // kWgrad: an arrival for each CTA's half (both by the leader's producer,
-            // or the last warp of each once the rows beyond the group are zero)
-            mbar_init(full0 + 8 * s, MODE == kWgrad ? 2 : 1);
+            mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
-            mbar_init(tail0 + 8 * s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(acc_full0 + 8 * a, 1);
@@ -474,15 +472,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                     break;
                 }
                 const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
-                uint32_t bar = map_to_rank(full0 + 8 * s, 0);
-                if (MODE == kWgrad && (kb + 1) * BK > t.rows) {
-                    // rows beyond the group: the last warp of each CTA hands its half on
-                    bar = map_to_rank(tail0 + 8 * s, rank);
-                    mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
-                } else if (leader) {
-                    mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
-                    if (MODE == kWgrad) mbar_arrive(full0 + 8 * s);  // for both halves
+                const uint32_t bar = map_to_rank(full0 + 8 * s, 0);
+                if constexpr (MODE == kWgrad) {
+                    const int live = t.rows - kb * BK;
+                    if (live < BK) {  // the group's last rows
+                        const int padded = (live + UMMA_K - 1) / UMMA_K * UMMA_K;
+                        if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * 4 * 128 * padded);
+                        int at = 0;
+                        const auto rows = [&](int h, int row) {  // 1 << h rows
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t to = sa + i * (A_BYTES / 2) + 128 * at;
+                                tma_load_2d_pair(to, &p.part_a[h], bar, t.m0 + 128 * (int)rank + 64 * i, row);
+                                tma_load_2d_pair(to + A_BYTES, &p.part_b[h], bar, t.n0 + 128 * (int)rank + 64 * i,
+                                                 row);
+                            }
+                            at += 1 << h;
+                        };
+#pragma unroll 1
+                        for (int h = 5; h >= 0; --h)
+                            if (live & (1 << h)) rows(h, t.r0 + kb * BK + at);
+#pragma unroll 1
+                        for (int h = 0; at < padded; ++h)  // beyond the tensor: zeros
+                            if (at & (1 << h)) rows(h, p.rows);
+                        continue;
+                    }
                 }
+                if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
                 if (MODE == kFc1) {
                     // 32 gate rows and the 32 up rows of the same features, twice
 #pragma unroll
@@ -547,11 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                 const int first = kb, last = kblocks - kb > seg_blocks ? kb + seg_blocks : kblocks;
                 for (; kb < last; ++kb, ++it) {
                     const int s = it % STAGES;
-                    // (a stage whose last rows were zeroed by both CTAs' threads: acquire
-                    // their writes)
-                    const bool zeroed = MODE == kWgrad && (kb + 1) * BK > t.rows;
-                    if (!(zeroed ? mbar_wait<true>(full0 + 8 * s, (it / STAGES) & 1)
-                                 : mbar_wait(full0 + 8 * s, (it / STAGES) & 1))) {
+                    if (!mbar_wait(full0 + 8 * s, (it / STAGES) & 1)) {
                         ok = false;
                         break;
                     }
@@ -559,6 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
                     const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+                        if (MODE == kWgrad && kb * BK + kk * UMMA_K >= t.rows) break;
                         // K-major: 16 elements along the swizzled row; MN-major: 16
                         // rows of 128 bytes, 64-element groups A_BYTES / 2 apart
                         const uint64_t a = kAMn ? smem_desc_128b(sa + kk * UMMA_K * 128, A_BYTES / 2)
@@ -797,34 +810,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 
             } while (kb < kblocks);
         }
         if (elect_one()) bulk_wait<0>();  // the stores, before their shared memory goes
-    } else if (MODE == kWgrad && warp == kScheduler + 1) {
-        // ---- zero the rows beyond the group in its last stage (both CTAs)
-        int it = 0;
-        uint32_t uses = 0;  // phase of each stage's tail barrier
-        for (int k = 0;; ++k) {
-            const Tile t = next_tile_warp(k);
-            if (t.group < 0) break;
-            it += blocks_of(t);
-            const int live = t.rows % BK;
-            if (live == 0) continue;
-            const int s = (it - 1) % STAGES;
-            if (!__all_sync(0xffffffffu, mbar_wait(tail0 + 8 * s, (uses >> s) & 1))) {
-                if (lane == 0) *abort_flag = 1;
-                break;
-            }
-            uses ^= 1u << s;
-            // four boxes of 64 rows of 128 bytes; the swizzle stays within a row
-            unsigned char *stage = smem + s * STAGE_BYTES;
-            for (int i = lane; i < (BK - live) * 8; i += 32) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    *reinterpret_cast<uint4 *>(stage + b * (A_BYTES / 2) + live * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-            }
-            // the zeros are for the tensor cores (async proxy)
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(full0 + 8 * s, 0));
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -1056,7 +1041,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
         const int quarter = warp & 3;
         float *part = reinterpret_cast<float *>(smem);
         if (MODE == kWgrad && last_rows != 0 && warp == 2) {
-            // zero the next group's rows in the last block, as in the pair kernel
+            // zero the next group's rows in the last block
             if (!__all_sync(0xffffffffu, mbar_wait(landed, 0)) && lane == 0) *abort_flag = 1;
             unsigned char *stage = smem + (kb1 - 1 - kb0) % kStages * kStage;
             for (int i = lane; i < (BK - last_rows) * 8; i += 32) {
@@ -1283,7 +1268,7 @@ swiglu_status_t launch_pairs(const Params &p, int64_t clusters, swiglu_stream_t 
         if (e != cudaSuccess) return moe::cuda_fail(e);
         if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true);
     }
-    e = moe::launch(grouped_mm_kernel<MODE>, dim3((unsigned)(2 * clusters)), kPairThreads<MODE>, SMEM_BYTES,
+    e = moe::launch(grouped_mm_kernel<MODE>, dim3((unsigned)(2 * clusters)), kPairThreads, SMEM_BYTES,
                     stream, 0, p);
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
@@ -1318,10 +1303,10 @@ swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_st
 // groups of equal size, which is all the host knows: operand bytes per SM at the
 // rates the two kernels reach, times the rounds of the grid, plus what a launch,
 // a tile and the joining of the sums take.  The constants are a fit to the times
-// of all five choices on 7,600 shapes (forward, fc1 and both gradients; 1 to
+// of all five choices on 12,200 shapes (forward, fc1 and both gradients; 1 to
 // 32768 rows, 1 to 64 groups, widths 64 to 14336); with them the choice is on
-// average 2.9 % slower than the best one, where always pairs are 22 % and always
-// one CTA per tile 31 % slower.
+// average 2.4 % slower than the best one, where always pairs are 19 % and always
+// one CTA per tile 44 % slower.
 struct Plan {
     int size;  // CTAs per tile of the split kernel; 0: pairs
 };
@@ -1333,17 +1318,17 @@ Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int spli
           int64_t least_size = 1) {
     const int64_t pair_n = rows_per < TILE_N ? ceil_div(rows_per, 32) * 32 : TILE_N;
     const int64_t pair_tiles = same * ceil_div(rows_per, TILE_N) * ceil_div(features, pair_f);
-    const int64_t pair_depth = kblocks * (A_BYTES + pair_n * BK) / 111;
+    const int64_t pair_depth = kblocks * (A_BYTES + pair_n * BK) / 112;
     Plan best = {0};
-    int64_t least = ceil_div(pair_tiles, kSms / 2) * (pair_depth > 1590 ? pair_depth : 1590) + 5570;
+    int64_t least = ceil_div(pair_tiles, kSms / 2) * (pair_depth > 1000 ? pair_depth : 1000) + 5920;
     const int64_t split_n = rows_per < nt ? ceil_div(rows_per, 16) * 16 : nt;
     const int64_t split_tiles = same * ceil_div(rows_per, nt) * ceil_div(features, split_f);
     for (int size = 1; size <= 8 && (size == 1 || 2 * size <= kblocks); size *= 2) {
         if (size < least_size) continue;
         const int64_t ctas = split_tiles * size;
         const int64_t bytes = ceil_div(kblocks, size) * (A_BYTES + split_n * BK * 2);
-        const int64_t time = (ctas <= kSms ? bytes / 102 : ceil_div(ctas, kSms) * bytes / 123) +
-                             ceil_div(ctas, 2 * kSms) * (3750 + 20 * split_n / size) + (size > 1 ? 1090 : 0);
+        const int64_t time = (ctas <= kSms ? bytes / 96 : ceil_div(ctas, kSms) * bytes / 111) +
+                             ceil_div(ctas, 2 * kSms) * (3850 + 69 * split_n / size) + (size > 1 ? 1250 : 0);
         if (time < least) {
             least = time;
             best.size = size;
@@ -1543,6 +1528,9 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK) ||
         !out_map(enc, &p.c, dw, eb, K, N, groups))
         return moe::cuda_fail(cudaErrorInvalidValue);
+    for (int h = 0; h < 6; ++h)
+        if (!map2(enc, &p.part_a[h], dy, N, rows, 1 << h) || !map2(enc, &p.part_b[h], x, K, rows, 1 << h))
+            return moe::cuda_fail(cudaErrorInvalidValue);
     p.features = (int)N;
     p.cols = (int)K;
     return launch_pairs<kWgrad>(p, pairs, stream);
