@@ -106,7 +106,7 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 
 struct Params {
     CUtensorMap a;     // the M side
-    CUtensorMap b[4];  // the N side, boxes of 16, 32, 64 and 128 rows (kWgrad: b[0] alone, 64 rows)
+    CUtensorMap b[8];  // the N side, boxes of 16, 32, 48, ... 128 rows (kWgrad: b[0] alone, 64 rows)
     CUtensorMap part_a[6], part_b[6];  // kWgrad, a group's last rows: boxes of 1, 2, ... 32 rows
     CUtensorMap c;     // the result (not kFc1), boxes of 64 bytes by 32 rows
     const int32_t *ends;
@@ -524,16 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         tma_load_2d_pair(sb + i * (A_BYTES / 2), &p.b[0], bar, t.n0 + 128 * (int)rank + 64 * i,
                                          t.r0 + kb * BK);
                 } else {
-                    int row = t.r0 + t.n0 + half * (int)rank;
-                    uint32_t dst = sb;
-#pragma unroll
-                    for (int i = 3; i >= 0; --i) {
-                        if (half & (16 << i)) {
-                            tma_load_2d_pair(dst, &p.b[i], bar, kb * BK, row);
-                            row += 16 << i;
-                            dst += (16 << i) * BK * 2;
-                        }
-                    }
+                    tma_load_2d_pair(sb, &p.b[half / 16 - 1], bar, kb * BK, t.r0 + t.n0 + half * (int)rank);
                 }
             }
         }
@@ -551,6 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (t.group < 0 || *abort_flag) break;
             const int kblocks = blocks_of(t);
             const uint32_t idesc = instr_desc(kAMn, kBMn, 256, width_of(t));
+            const int deep = MODE == kWgrad ? t.rows : p.depth;
             int kb = 0;
             do {  // one accumulation
                 const int acc = lt & 1;
@@ -571,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < BK / UMMA_K; ++kk) {
-                        if (MODE == kWgrad && kb * BK + kk * UMMA_K >= t.rows) break;
+                        if (kb * BK + kk * UMMA_K >= deep) break;
                         // K-major: 16 elements along the swizzled row; MN-major: 16
                         // rows of 128 bytes, 64-element groups A_BYTES / 2 apart
                         const uint64_t a = kAMn ? smem_desc_128b(sa + kk * UMMA_K * 128, A_BYTES / 2)
@@ -1002,16 +994,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
                     tma_load_2d(sa + A_BYTES + i * (A_BYTES / 2), &p.b[0], bar, t.n0 + 64 * i, t.r0 + kb * BK);
                 continue;
             }
-            int row = t.r0 + t.n0;
-            uint32_t dst = sa + A_BYTES;
-#pragma unroll
-            for (int i = 3; i >= 0; --i) {
-                if ((16 << i) <= NT && (width & (16 << i))) {
-                    tma_load_2d(dst, &p.b[i], bar, kb * BK, row);
-                    row += 16 << i;
-                    dst += (16 << i) * BK * 2;
-                }
-            }
+            tma_load_2d(sa + A_BYTES, &p.b[width / 16 - 1], bar, kb * BK, t.r0 + t.n0);
         }
     } else if (warp == 1 && kb1 > kb0 && elect_one()) {
         const uint32_t idesc = instr_desc(kAMn, kBMn, 128, width);
@@ -1244,12 +1227,13 @@ bool out_map(EncodeTiled enc, CUtensorMap *map, void *p, int eb, int64_t inner, 
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The N side of the products over rows: boxes of 16, 32, 64 and 128 rows, as far
+// The N side of the products over rows: boxes of 16, 32, 48, ... 128 rows, as far
 // as a tile of `rows` rows (to 16) can need them; a CTA of a pair loads half of
-// its tile (to 32), which is no more.
+// its tile (to 32), which is no more.  One box whatever the width: with boxes of
+// powers of two, up to three loads, 10739 rows by [4096, 2048] took 1 % longer.
 bool row_maps(EncodeTiled enc, CUtensorMap *maps, const void *p, int64_t inner, int64_t rows) {
-    for (int i = 0; i < 4 && (i == 0 || 16 << i <= (rows + 15) / 16 * 16); ++i)
-        if (!map2(enc, maps + i, p, inner, rows, 16 << i)) return false;
+    for (int i = 0; i < 8 && 16 * i < rows; ++i)
+        if (!map2(enc, maps + i, p, inner, rows, 16 * (i + 1))) return false;
     return true;
 }
 
