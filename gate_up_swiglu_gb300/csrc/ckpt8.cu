@@ -35,10 +35,7 @@ bool multiple(int64_t by, std::initializer_list<int64_t> v) {
 template <int BYTES>
 constexpr int kFwdPacks = BYTES >= 32 ? 1 : 2;
 
-// Blocks of 32 columns a warp of the single-element kernels takes at a time.
-constexpr int kNarrowFwd = 8, kNarrowBwd = 4;
-
-// The weighted backward: packs (or groups of four elements) of a row that one
+// The weighted backward: packs (or groups of narrow ones) of a row that one
 // warp takes ([16384, 2 x 256] bf16 22 -> 12 us against a CTA per row), and the
 // CTAs up to which rows are shared by clusters (one row of n = 28008 fp32 23 -> 9 us).
 // 16-byte packs take CTAs of 256 threads ([8192, 2 x 14344] bf16 175 -> 153 us; 32-byte
@@ -57,12 +54,12 @@ template <typename E, int VEC>
 swiglu_status_t launch_fwd(ckpt8::FwdParams p, swiglu_stream_t stream) {
     constexpr int T = 128;
     cudaError_t e;
-    if constexpr (VEC == 1) {
-        constexpr int K = kNarrowFwd;
-        p.row_packs = (int32_t)((p.n + 32 * K - 1) / (32 * K));
+    if constexpr (ckpt8::kNarrow<E, VEC>) {
+        constexpr int K = ckpt8::kFwdChunks<VEC>;
+        p.row_packs = (int32_t)((p.n + 32 * VEC * K - 1) / (32 * VEC * K));
         p.packs = p.rows * p.row_packs;
         p.div = make_fast_div((uint64_t)p.row_packs);
-        e = moe::launch(ckpt8::ckpt8_fwd_narrow_kernel<E, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, 0, p);
+        e = moe::launch(ckpt8::ckpt8_fwd_narrow_kernel<E, VEC, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, 0, p);
     } else {
         p.row_packs = p.blocks * (ckpt8::kBlock / VEC);
         p.packs = p.rows * p.row_packs;
@@ -83,7 +80,8 @@ swiglu_status_t launch_bwd(ckpt8::BwdParams p, swiglu_stream_t stream) {
     if (p.dw != nullptr) {
         // a warp per row of up to kWarpRow packs, else a CTA, or a cluster while that
         // gives the SMs more to do
-        const int64_t packs = VEC == 1 ? (p.n + 3) / 4 : p.row_packs;
+        const int64_t packs =
+            ckpt8::kNarrow<E, VEC> ? (p.row_packs + ckpt8::kBwdChunks - 1) / ckpt8::kBwdChunks : p.row_packs;
         if (packs <= kWarpRow) {
             const int64_t ctas = (p.rows + T / 32 - 1) / (T / 32);
             e = moe::launch(ckpt8::ckpt8_bwd_weighted_kernel<E, VEC, T, T / 32>,
@@ -96,23 +94,23 @@ swiglu_status_t launch_bwd(ckpt8::BwdParams p, swiglu_stream_t stream) {
             e = moe::launch(ckpt8::ckpt8_bwd_weighted_kernel<E, VEC, TR, 1>, dim3((unsigned)(ctas * size)), TR, 0,
                             stream, size, p);
         }
-    } else if constexpr (VEC == 1) {
-        constexpr int K = kNarrowBwd;
-        p.row_packs = (int32_t)((p.n + 32 * K - 1) / (32 * K));
+    } else if constexpr (ckpt8::kNarrow<E, VEC>) {
+        constexpr int K = ckpt8::kBwdChunks;
+        p.row_packs = (int32_t)((p.n + 32 * VEC * K - 1) / (32 * VEC * K));
         p.packs = p.rows * p.row_packs;
         p.div = make_fast_div((uint64_t)p.row_packs);
-        e = moe::launch(ckpt8::ckpt8_bwd_narrow_kernel<E, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, 0, p);
+        e = moe::launch(ckpt8::ckpt8_bwd_narrow_kernel<E, VEC, K, T>, dim3(one_pass(p.packs, T / 32)), T, 0, stream, 0, p);
     } else {
         e = moe::launch(ckpt8::ckpt8_bwd_kernel<E, VEC, T>, dim3(one_pass(p.packs, T)), T, 0, stream, 0, p);
     }
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
 
-// Elements of the widest pack (32 or 16 bytes) that n, the tensors' strides
+// Elements of the widest pack (32 to 4 bytes, two elements at least) that n, the tensors' strides
 // (elements) and addresses and the codes' stride and address allow, else 1.
 int pick_vec(int eb, int64_t n, std::initializer_list<int64_t> strides, std::initializer_list<int64_t> addresses,
              int64_t q_stride, const void *q) {
-    for (int bytes = 32; bytes >= 16; bytes /= 2) {
+    for (int bytes = 32; bytes >= 2 * eb; bytes /= 2) {
         const int vec = bytes / eb;
         if (n % vec == 0 && multiple(vec, strides) && multiple(bytes, addresses) && q_stride % vec == 0 &&
             (uintptr_t)q % (uintptr_t)vec == 0)
@@ -162,10 +160,13 @@ swiglu_status_t swiglu_ckpt8_fwd(const void *x, const float *w, void *y, void *q
     if (dtype == SWIGLU_BF16) {
         if (vec == 16) return launch_fwd<swiglu::BF16, 16>(p, stream);
         if (vec == 8) return launch_fwd<swiglu::BF16, 8>(p, stream);
+        if (vec == 4) return launch_fwd<swiglu::BF16, 4>(p, stream);
+        if (vec == 2) return launch_fwd<swiglu::BF16, 2>(p, stream);
         return launch_fwd<swiglu::BF16, 1>(p, stream);
     }
     if (vec == 8) return launch_fwd<swiglu::F32, 8>(p, stream);
     if (vec == 4) return launch_fwd<swiglu::F32, 4>(p, stream);
+    if (vec == 2) return launch_fwd<swiglu::F32, 2>(p, stream);
     return launch_fwd<swiglu::F32, 1>(p, stream);
 }
 
@@ -224,10 +225,13 @@ swiglu_status_t swiglu_ckpt8_bwd(const void *dy, const void *q, const void *scal
     if (dtype == SWIGLU_BF16) {
         if (vec == 16) return launch_bwd<swiglu::BF16, 16>(p, stream);
         if (vec == 8) return launch_bwd<swiglu::BF16, 8>(p, stream);
+        if (vec == 4) return launch_bwd<swiglu::BF16, 4>(p, stream);
+        if (vec == 2) return launch_bwd<swiglu::BF16, 2>(p, stream);
         return launch_bwd<swiglu::BF16, 1>(p, stream);
     }
     if (vec == 8) return launch_bwd<swiglu::F32, 8>(p, stream);
     if (vec == 4) return launch_bwd<swiglu::F32, 4>(p, stream);
+    if (vec == 2) return launch_bwd<swiglu::F32, 2>(p, stream);
     return launch_bwd<swiglu::F32, 1>(p, stream);
 }
 

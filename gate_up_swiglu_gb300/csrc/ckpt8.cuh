@@ -104,6 +104,23 @@ __device__ __forceinline__ void decode(const uint32_t *q, float f, float *v) {
     }
 }
 
+// VEC codes.
+template <int VEC>
+__device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t *q) {
+    if constexpr (VEC == 1)
+        q[0] = __ldg(p);
+    else
+        swiglu::Ld<VEC, swiglu::kLdNC>::run(p, q);
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t *q) {
+    if constexpr (VEC == 1)
+        *p = (uint8_t)q[0];
+    else
+        swiglu::St<VEC, swiglu::kStStream>::run(p, q);
+}
+
 // ---------------------------------------------------------------- kernels ---
 // Both are one pass over the data: the forward reads x (2 elements a pair) and
 // writes y, two codes and 2/32 scale bytes; the backward reads dy, the codes
@@ -185,8 +202,8 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
                 encode<VEC>(g, encode_factor(cg), qg);
                 encode<VEC>(u, encode_factor(cu), qu);
                 uint8_t *qr = p.q + row[k] * p.q_stride + col[k];
-                swiglu::St<VEC, swiglu::kStStream>::run(qr, qg);
-                swiglu::St<VEC, swiglu::kStStream>::run(qr + p.n, qu);
+                store_codes<VEC>(qr, qg);
+                store_codes<VEC>(qr + p.n, qu);
                 if (col[k] % kBlock == 0) {
                     uint8_t *sr = p.scales + row[k] * p.s_stride + col[k] / kBlock;
                     sr[0] = (uint8_t)cg;
@@ -206,94 +223,165 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
     }
 }
 
-// ------------------------------------------------------ single elements ---
-// Odd n, or rows misaligned to one another: every operand moves element by
-// element.  A warp takes K blocks of 32 columns of one row, one lane per column,
-// so a block's maximum is one warp-wide reduction, each lane forms its row
-// pointers once for K elements, and all loads are issued before the first is
-// used: [3000, 2 x 5503] fp32 with weights forward 56 us (0.62 of copy; one element
-// per thread over the flattened index, with shuffles for the maximum, 131 us),
-// backward 56 us.  The memory instructions bound it: seven per 32 pairs, of 32 to
-// 128 bytes each, however few the others (bf16 [8192, 2 x 5503] 132 us, 0.41).
+// --------------------------------------------------------- narrow packs ---
+// Widths, strides or addresses that allow packs of at most 8 bytes, down to single
+// elements (odd n, or rows misaligned to one another).  A warp takes K chunks of
+// 32 VEC columns of one row, one pack per lane and chunk, so a block is 32 / VEC
+// lanes (single elements: the warp, whose maximum is one reduction), each lane
+// forms its row pointers once for K packs, and all loads are issued before the
+// first is used (one pack per thread over the flattened index, as for wide packs,
+// was 1.2 to 2.3 times slower).  Forward and backward without weights, of the 6680
+// GB/s copy: packs of 8 bytes bf16 [8192, 2 x 5460] 66 us (0.82) and 62 us (0.87),
+// fp32 [8192, 2 x 2730] 61 us (0.77) and 57 us (0.83); of 4 bytes [8192, 2 x 10922]
+// 164 us (0.66) and 147 us (0.73); elements bf16 [8192, 2 x 5503] 126 us (0.43) and
+// 108 us (0.50), fp32 [3000, 2 x 5503] 51.6 us (0.67) and 50.8 us (0.68).  The fewer
+// bytes a memory instruction moves the more it is these that bound them: taking
+// arithmetic out of the single elements gained 1 %.
+
+template <typename E, int VEC>
+constexpr bool kNarrow = E::kBytes * VEC <= 8;
+
+// Chunks of 32 packs a warp takes at a time (4-byte packs forward: 6 chunks 164 us, 4
+// 181 us, 8 165 us; backward: 6 147 us, 4 150 us, 8 142 us, but 73 against 65 us for
+// weighted packs of 8 bytes).
+template <int VEC>
+constexpr int kFwdChunks = VEC == 1 ? 8 : VEC == 2 ? 6 : 4;
+constexpr int kBwdChunks = 6;
 
 // Positions of a warp: its row and the first column of its lane.
 struct Segment {
     int64_t row, col;
 };
 
-template <int K>
+template <int VEC, int K>
 __device__ __forceinline__ Segment segment_at(int64_t seg, int32_t chunks, const swiglu::FastDiv &div) {
     const int64_t r = swiglu::fast_div(seg, div);
-    return {r, (seg - r * chunks) * (32 * K) + (threadIdx.x & 31)};
+    return {r, (seg - r * chunks) * (32 * VEC * K) + (threadIdx.x & 31) * VEC};
 }
 
-// The scale code of the warp's 32 values (a block), from the bits of |v|, which
-// order like the values; `plain`: none is infinite, NaN or above 1.75 * 2^127, so
-// that encoding needs no care.
-struct BlockCode {
-    uint32_t code;
-    bool plain;
-};
-
-__device__ __forceinline__ BlockCode warp_code(float v) {
-    const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
-    uint32_t m = __reduce_max_sync(0xffffffffu, b);
-    const bool plain = m <= 0x7f600000u;
-    if (!plain) m = __reduce_max_sync(0xffffffffu, b < 0x7f800000u ? b : 0u);
-    return {scale_code(__uint_as_float(m)), plain};
+// Packs of this lane (<= 0: none).
+template <int VEC, int K>
+__device__ __forceinline__ int live_packs(const Segment &at, int64_t n) {
+    return (int)min((int64_t)K, (n - at.col + 32 * VEC - 1) / (32 * VEC));
 }
 
-// p.row_packs: warps (segments of 32 K columns) per row; p.packs: in all.
-template <typename E, int K, int T>
+// The largest of the lanes of a block, for the gates and the ups (bits of |v|; those
+// of bf16 values are 16 and travel together).
+template <typename E, int VEC>
+__device__ __forceinline__ void block_max(uint32_t &g, uint32_t &u) {
+    if (VEC == 1) {
+        g = __reduce_max_sync(0xffffffffu, g);
+        u = __reduce_max_sync(0xffffffffu, u);
+    } else if (E::kBytes == 2) {
+        uint32_t both = (g >> 16) | u;
+#pragma unroll
+        for (int o = 16 / VEC; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
+        g = both << 16;
+        u = both & 0xffff0000u;
+    } else {
+#pragma unroll
+        for (int o = 16 / VEC; o > 0; o >>= 1) {
+            g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+            u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
+        }
+    }
+}
+
+// The scale codes of a block, from the bits of |v|, which order like the values.
+// True: no value of the warp is infinite, NaN or above 1.75 * 2^127, so that encoding
+// needs no care.
+template <typename E, int VEC>
+__device__ __forceinline__ bool block_codes(const float *g, const float *u, uint32_t &cg, uint32_t &cu) {
+    constexpr uint32_t kAbs = 0x7fffffffu, kInf = 0x7f800000u;
+    uint32_t mg = 0u, mu = 0u;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        mg = max(mg, __float_as_uint(g[i]) & kAbs);
+        mu = max(mu, __float_as_uint(u[i]) & kAbs);
+    }
+    block_max<E, VEC>(mg, mu);
+    const bool plain = !__any_sync(0xffffffffu, max(mg, mu) > 0x7f600000u);
+    if (!plain) {
+        mg = mu = 0u;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const uint32_t a = __float_as_uint(g[i]) & kAbs, b = __float_as_uint(u[i]) & kAbs;
+            mg = max(mg, a < kInf ? a : 0u);
+            mu = max(mu, b < kInf ? b : 0u);
+        }
+        block_max<E, VEC>(mg, mu);
+    }
+    cg = scale_code(__uint_as_float(mg));
+    cu = scale_code(__uint_as_float(mu));
+    return plain;
+}
+
+// p.row_packs: warps (segments of 32 VEC K columns) per row; p.packs: in all.
+template <typename E, int VEC, int K, int T>
 __global__ void __launch_bounds__(T) ckpt8_fwd_narrow_kernel(const FwdParams p) {
     swiglu::await_previous_grid();
     swiglu::allow_next_grid();
-    constexpr int EB = E::kBytes;
+    constexpr int EB = E::kBytes, B = EB * VEC, NW = (B + 3) / 4, W = 32 * VEC;
+    const int lane = threadIdx.x & 31;
     for (int64_t seg = (int64_t)blockIdx.x * (T / 32) + (threadIdx.x >> 5); seg < p.packs;
          seg += (int64_t)gridDim.x * (T / 32)) {
-        const Segment at = segment_at<K>(seg, p.row_packs, p.div);
+        const Segment at = segment_at<VEC, K>(seg, p.row_packs, p.div);
         const char *xr = p.x + at.row * p.x_stride + at.col * EB;
         const char *ur = xr + p.n * EB;
-        const int live = (int)min((int64_t)K, (p.n - at.col + 31) / 32);  // elements of this lane (<= 0: none)
-        uint32_t g[K], u[K];
+        const int live = live_packs<VEC, K>(at, p.n);
+        uint32_t gw[K][NW], uw[K][NW];
 #pragma unroll
         for (int i = 0; i < K; ++i) {
-            g[i] = u[i] = 0u;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) gw[i][k] = uw[i][k] = 0u;
             if (i < live) {
-                swiglu::Ld<EB, swiglu::kLdNC>::run(xr + i * 32 * EB, &g[i]);
-                swiglu::Ld<EB, swiglu::kLdNC>::run(ur + i * 32 * EB, &u[i]);
+                swiglu::Ld<B, swiglu::kLdNC>::run(xr + i * W * EB, gw[i]);
+                swiglu::Ld<B, swiglu::kLdNC>::run(ur + i * W * EB, uw[i]);
             }
         }
         const float wr = p.w != nullptr ? __ldg(p.w + at.row) : 1.0f;
         char *yr = p.y + at.row * p.y_stride + at.col * EB;
         uint8_t *qr = p.q + at.row * p.q_stride + at.col;
         uint8_t *sr = p.scales + at.row * p.s_stride + at.col / kBlock;
-        const int64_t first = at.col - (threadIdx.x & 31);
+        const int64_t first = at.col - lane * VEC;
 #pragma unroll
         for (int i = 0; i < K; ++i) {
-            if (first + 32 * i >= p.n) break;  // the same for the whole warp
-            const float gf = E::get(&g[i], 0), uf = E::get(&u[i], 0);
-            const BlockCode cg = warp_code(gf), cu = warp_code(uf);
-            const float fg = encode_factor(cg.code), fu = encode_factor(cu.code);
-            if (i < live) {
-                uint32_t q = codes2(__fmul_rn(gf, fg), __fmul_rn(uf, fu));
-                if (!(cg.plain && cu.plain)) {
-                    uint32_t qg, qu;
-                    encode<1>(&gf, fg, &qg);
-                    encode<1>(&uf, fu, &qu);
-                    q = qg | qu << 8;
-                }
-                qr[i * 32] = (uint8_t)q;
-                qr[p.n + i * 32] = (uint8_t)(q >> 8);
-                const swiglu::Act act = swiglu::activation<E, false, true>(gf);
-                const float y = __fmul_rn(__fmul_rn(__fmul_rn(act.silu, uf), wr), act.scale);
-                uint32_t o = 0u;
-                E::put(&o, 0, y);
-                swiglu::St<EB, swiglu::kStStream>::run(yr + i * 32 * EB, &o);
+            if (first + W * i >= p.n) break;  // the same for the whole warp
+            float g[VEC], u[VEC];
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                g[k] = E::get(gw[i], k);
+                u[k] = E::get(uw[i], k);
             }
-            if ((threadIdx.x & 31) == 0) {
-                sr[i] = (uint8_t)cg.code;
-                sr[i + p.blocks] = (uint8_t)cu.code;
+            uint32_t cg, cu;
+            const bool plain = block_codes<E, VEC>(g, u, cg, cu);
+            const float fg = encode_factor(cg), fu = encode_factor(cu);
+            if (i < live) {
+                uint32_t qg, qu;
+                if (VEC == 1 && plain) {
+                    qg = codes2(__fmul_rn(g[0], fg), __fmul_rn(u[0], fu));
+                    qu = qg >> 8;
+                } else if (plain) {
+                    encode_values<VEC, false>(g, fg, &qg);
+                    encode_values<VEC, false>(u, fu, &qu);
+                } else {
+                    encode_values<VEC, true>(g, fg, &qg);
+                    encode_values<VEC, true>(u, fu, &qu);
+                }
+                store_codes<VEC>(qr + i * W, &qg);
+                store_codes<VEC>(qr + p.n + i * W, &qu);
+                float yv[VEC];
+                if (E::kDeepScale && (swiglu::pack_has_deep<E, VEC>(gw[i])))
+                    swiglu::fwd_pack<E, VEC, swiglu::kWeight, true>(gw[i], uw[i], nullptr, nullptr, wr, yv);
+                else
+                    swiglu::fwd_pack<E, VEC, swiglu::kWeight, false>(gw[i], uw[i], nullptr, nullptr, wr, yv);
+                uint32_t o[NW] = {};
+                swiglu::store_pack<E, VEC>(o, yv);
+                swiglu::St<B, swiglu::kStStream>::run(yr + i * W * EB, o);
+                if (lane * VEC % kBlock == 0) {
+                    sr[i * VEC] = (uint8_t)cg;
+                    sr[i * VEC + p.blocks] = (uint8_t)cu;
+                }
             }
         }
     }
@@ -344,46 +432,46 @@ __device__ __forceinline__ void bwd_values(const uint32_t *d, const float *g, co
     }
 }
 
-// What a pack reads.
+// What a pack reads.  It lies `at` packs (whole blocks, known to the compiler) behind
+// column col of row r.  (Pointers formed once for both halves of the work held 7 more
+// registers and were 3 % slower with one pack per thread.)
 template <typename E, int VEC>
 struct BwdPack {
     static constexpr int B = E::kBytes * VEC;
     uint32_t d[(B + 3) / 4], qg[(VEC + 3) / 4], qu[(VEC + 3) / 4], cg, cu;
 
-    __device__ __forceinline__ void load(const BwdParams &p, int64_t r, int32_t c) {
-        const int64_t col = (int64_t)c * VEC;
+    __device__ __forceinline__ void load(const BwdParams &p, int64_t r, int64_t col, int at) {
         const uint8_t *qr = p.q + r * p.q_stride + col;
         const uint8_t *sr = p.scales + r * p.s_stride + col / kBlock;
-        swiglu::Ld<B, swiglu::kLdNC>::run(p.dy + r * p.dy_stride + col * E::kBytes, d);
-        swiglu::Ld<VEC, swiglu::kLdNC>::run(qr, qg);
-        swiglu::Ld<VEC, swiglu::kLdNC>::run(qr + p.n, qu);
-        cg = __ldg(sr);
-        cu = __ldg(sr + p.blocks);
+        swiglu::Ld<B, swiglu::kLdNC>::run(p.dy + r * p.dy_stride + col * E::kBytes + at * B, d);
+        load_codes<VEC>(qr + at * VEC, qg);
+        load_codes<VEC>(qr + p.n + at * VEC, qu);
+        cg = __ldg(sr + at * VEC / kBlock);
+        cu = __ldg(sr + p.blocks + at * VEC / kBlock);
     }
 
     template <int MODE>
-    __device__ __forceinline__ void finish(const BwdParams &p, int64_t r, int32_t c, float wr, float &acc) const {
-        const int64_t col = (int64_t)c * VEC;
+    __device__ __forceinline__ void finish(const BwdParams &p, int64_t r, int64_t col, int at, float wr,
+                                           float &acc) const {
         float g[VEC], u[VEC], dg[VEC], du[VEC], yv[VEC];
         decode<VEC>(qg, decode_factor(cg), g);
         decode<VEC>(qu, decode_factor(cu), u);
         float gmin = g[0];
 #pragma unroll
         for (int i = 1; i < VEC; ++i) gmin = fminf(gmin, g[i]);
-        if (E::kDeepScale && gmin < -64.0f)
+        if (E::kDeepScale && (gmin < -64.0f))
             bwd_values<E, VEC, MODE, true>(d, g, u, wr, acc, dg, du, yv);
         else
             bwd_values<E, VEC, MODE, false>(d, g, u, wr, acc, dg, du, yv);
-        uint32_t o[(B + 3) / 4] = {};
-        swiglu::store_pack<E, VEC>(o, dg);
+        const auto store = [](char *to, const float *v) {
+            uint32_t o[(B + 3) / 4] = {};
+            swiglu::store_pack<E, VEC>(o, v);
+            swiglu::St<B, swiglu::kStStream>::run(to, o);
+        };
         char *dxr = p.dx + r * p.dx_stride + col * E::kBytes;
-        swiglu::St<B, swiglu::kStStream>::run(dxr, o);
-        swiglu::store_pack<E, VEC>(o, du);
-        swiglu::St<B, swiglu::kStStream>::run(dxr + p.n * E::kBytes, o);
-        if (p.y != nullptr) {
-            swiglu::store_pack<E, VEC>(o, yv);
-            swiglu::St<B, swiglu::kStStream>::run(p.y + r * p.y_stride + col * E::kBytes, o);
-        }
+        store(dxr + at * B, dg);
+        store(dxr + p.n * E::kBytes + at * B, du);
+        if (p.y != nullptr) store(p.y + r * p.y_stride + col * E::kBytes + at * B, yv);
     }
 };
 
@@ -397,65 +485,32 @@ __global__ void __launch_bounds__(T) ckpt8_bwd_kernel(const BwdParams p) {
         const int64_t r = swiglu::fast_div(v, p.div);
         const int32_t c = (int32_t)(v - r * p.row_packs);
         BwdPack<E, VEC> pack;
-        pack.load(p, r, c);
-        pack.template finish<swiglu::kPlain>(p, r, c, 1.0f, acc);
+        pack.load(p, r, (int64_t)c * VEC, 0);
+        pack.template finish<swiglu::kPlain>(p, r, (int64_t)c * VEC, 0, 1.0f, acc);
     }
 }
 
-// K elements of one lane (columns col, col + 32, ...), all loads first.
-template <typename E, int K, int MODE>
-__device__ __forceinline__ void bwd_elements(const BwdParams &p, const Segment &at, float wr, float &acc) {
-    constexpr int EB = E::kBytes;
-    const int live = (int)min((int64_t)K, (p.n - at.col + 31) / 32);
-    const char *dyr = p.dy + at.row * p.dy_stride + at.col * EB;
-    const uint8_t *qr = p.q + at.row * p.q_stride + at.col;
-    const uint8_t *ur = qr + p.n;
-    const uint8_t *sr = p.scales + at.row * p.s_stride + at.col / kBlock;
-    uint32_t d[K], qg[K], qu[K], cg[K], cu[K];
+// K packs of one lane (columns col, col + 32 VEC, ...), all loads first.
+template <typename E, int VEC, int K, int MODE>
+__device__ __forceinline__ void bwd_packs(const BwdParams &p, const Segment &at, float wr, float &acc) {
+    const int live = live_packs<VEC, K>(at, p.n);
+    BwdPack<E, VEC> pack[K];
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-        if (i < live) {
-            swiglu::Ld<EB, swiglu::kLdNC>::run(dyr + i * 32 * EB, &d[i]);
-            qg[i] = qr[i * 32];
-            qu[i] = ur[i * 32];
-            cg[i] = sr[i];
-            cu[i] = sr[i + p.blocks];
-        }
-    }
-    char *dgr = p.dx + at.row * p.dx_stride + at.col * EB;
-    char *dur = dgr + p.n * EB;
-    char *yr = p.y + at.row * p.y_stride + at.col * EB;
+    for (int i = 0; i < K; ++i)
+        if (i < live) pack[i].load(p, at.row, at.col, 32 * i);
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-        if (i < live) {
-            const uint32_t both = qg[i] | qu[i] << 8;
-            float gu[2], dg, du, y;
-            decode<2>(&both, 1.0f, gu);
-            const float g = __fmul_rn(gu[0], decode_factor(cg[i])), u = __fmul_rn(gu[1], decode_factor(cu[i]));
-            bwd_values<E, 1, MODE, E::kDeepScale>(&d[i], &g, &u, wr, acc, &dg, &du, &y);
-            uint32_t o = 0u;
-            E::put(&o, 0, dg);
-            swiglu::St<EB, swiglu::kStStream>::run(dgr + i * 32 * EB, &o);
-            o = 0u;
-            E::put(&o, 0, du);
-            swiglu::St<EB, swiglu::kStStream>::run(dur + i * 32 * EB, &o);
-            if (p.y != nullptr) {
-                o = 0u;
-                E::put(&o, 0, y);
-                swiglu::St<EB, swiglu::kStStream>::run(yr + i * 32 * EB, &o);
-            }
-        }
-    }
+    for (int i = 0; i < K; ++i)
+        if (i < live) pack[i].template finish<MODE>(p, at.row, at.col, 32 * i, wr, acc);
 }
 
-template <typename E, int K, int T>
+template <typename E, int VEC, int K, int T>
 __global__ void __launch_bounds__(T) ckpt8_bwd_narrow_kernel(const BwdParams p) {
     swiglu::await_previous_grid();
     swiglu::allow_next_grid();
     float acc = 0.0f;
     for (int64_t seg = (int64_t)blockIdx.x * (T / 32) + (threadIdx.x >> 5); seg < p.packs;
          seg += (int64_t)gridDim.x * (T / 32))
-        bwd_elements<E, K, swiglu::kPlain>(p, segment_at<K>(seg, p.row_packs, p.div), 1.0f, acc);
+        bwd_packs<E, VEC, K, swiglu::kPlain>(p, segment_at<VEC, K>(seg, p.row_packs, p.div), 1.0f, acc);
 }
 
 // With weights a row's dw is one sum, in an order that the sizes fix.  ROWS = 4:
@@ -482,16 +537,16 @@ __global__ void __launch_bounds__(T, E::kBytes * VEC == 32 && T == 128 ? 8 : 0) 
     for (int64_t r = (int64_t)(blockIdx.x / size) * ROWS + (ROWS == 1 ? 0 : warp); r < p.rows; r += rows_at_once) {
         const float wr = __ldg(p.w + r);
         float acc = 0.0f;
-        if constexpr (VEC == 1) {
-            constexpr int K = 4;
-            for (int64_t c = (int64_t)(id >> 5) * (32 * K); c < p.n; c += (int64_t)threads * K)
-                bwd_elements<E, K, swiglu::kWeight>(p, {r, c + lane}, wr, acc);
+        if constexpr (kNarrow<E, VEC>) {
+            constexpr int K = kBwdChunks;
+            for (int64_t c = (int64_t)(id >> 5) * (32 * VEC * K); c < p.n; c += (int64_t)threads * (VEC * K))
+                bwd_packs<E, VEC, K, swiglu::kWeight>(p, {r, c + lane * VEC}, wr, acc);
         } else {
             // (two packs in flight held 96 registers and were 5-13 % slower in bf16)
             for (int32_t c = id; c < p.row_packs; c += threads) {
                 BwdPack<E, VEC> pack;
-                pack.load(p, r, c);
-                pack.template finish<swiglu::kWeight>(p, r, c, wr, acc);
+                pack.load(p, r, (int64_t)c * VEC, 0);
+                pack.template finish<swiglu::kWeight>(p, r, (int64_t)c * VEC, 0, wr, acc);
             }
         }
 #pragma unroll

@@ -9,6 +9,8 @@ Tolerances (fixed before the first run):
     (2^-17 for bf16's hardware exponential and reciprocal, 2e-6 or 1e-7 each for
     fp32) and one step of fp32.
 """
+import math
+
 import pytest
 import torch
 
@@ -208,6 +210,45 @@ def test_strides_and_guards(sw, n, pads, dt):
     assert_parity(dxv, rdx.to(DT[dt]), "dx")
     assert_parity(y2v, ry.to(DT[dt]), "y")
     assert _untouched(bdx, rows, 2 * n, 2 * n + px) and _untouched(by2, rows, n, n + py)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [2, 4, 34, 36, 62, 66, 68, 100, 126, 250, 252, 260, 1030, 2730, 5460])
+def test_narrow_packs(sw, n, dt):
+    """Widths of packs of 8 and 4 bytes; from an odd column on, of single elements: the
+    same codes and bits either way, with values of every care in some rows."""
+    rows = 9
+    x = _x(rows, n, dt, 31 * n, std=2.0)
+    x[1, 0], x[2, n], x[3, n - 1], x[4, 2 * n - 1], x[5, n // 2] = math.inf, -math.inf, math.nan, 3e38, -90.0
+    x[6] = 0.0
+    w = torch.rand(rows, generator=torch.Generator().manual_seed(n)).cuda()
+    dy = torch.randn(rows, n, generator=torch.Generator().manual_seed(n + 1)).to(DT[dt])
+    results = []
+    for off in (0, 1):
+        xv = torch.zeros(rows, 2 * n + 8, dtype=DT[dt], device="cuda")[:, off:off + 2 * n]
+        xv.copy_(x)
+        dyv = torch.zeros(rows, n + 8, dtype=DT[dt], device="cuda")[:, off:off + n]
+        dyv.copy_(dy)
+        y, q, scales = sw.swiglu_ckpt8_fwd(xv, w)
+        _check_codes(q, scales, x, f"{dt} n {n} from column {off}")
+        assert_bitwise(y, sw.swiglu_gateup_weighted_fwd(x.cuda(), w), "y")
+        plain = sw.swiglu_ckpt8_bwd(dyv, q, scales, None, return_y=True)
+        weighted = sw.swiglu_ckpt8_bwd(dyv, q, scales, w, return_y=True)
+        results.append((q.view(torch.uint8), plain[0], plain[2], weighted[0], weighted[2]))
+        usual = [0, 5, 6, 7, 8]
+        xr = R.restored(q.cpu(), scales.cpu())[usual]
+        rdx, rdw, ry, rabs = R.swiglu_bwd(dy[usual], xr, w.cpu()[usual])
+        assert_parity(weighted[0][usual], rdx.to(DT[dt]), "dx")
+        assert_parity(weighted[2][usual], ry.to(DT[dt]), "y")
+        tol = (n / 32 + 16) * 2.0 ** -24 * rabs + 2.0 ** -23 * rdw.abs()
+        tol += 2.0 ** -17 * rabs if dt == "bf16" else 2e-6 * rabs + n * 1e-7
+        assert bool(((weighted[1].cpu().double()[usual] - rdw).abs() <= tol).all()), "dw"
+    for a, b in zip(*results):
+        if a.dtype == torch.uint8:
+            assert torch.equal(a, b)
+        else:
+            nan = a.isnan()
+            assert torch.equal(nan, b.isnan()) and torch.equal(a[~nan], b[~nan])
 
 
 def test_three_dimensions_streams_and_repeats(sw):
