@@ -1290,10 +1290,10 @@ swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_st
 // groups of equal size, which is all the host knows: operand bytes per SM at the
 // rates the two kernels reach, times the rounds of the grid, plus what a launch,
 // a tile and the joining of the sums take.  The constants are a fit to the times
-// of all five choices on 12,200 shapes (forward, fc1 and both gradients; 1 to
+// of all five choices on 14,000 shapes (forward, fc1 and both gradients; 1 to
 // 32768 rows, 1 to 64 groups, widths 64 to 14336); with them the choice is on
-// average 2.4 % slower than the best one, where always pairs are 19 % and always
-// one CTA per tile 44 % slower.
+// average 2.3 % slower than the best one, where always pairs are 20 % and always
+// one CTA per tile 47 % slower.
 struct Plan {
     int size;  // CTAs per tile of the split kernel; 0: pairs
 };
