@@ -9,6 +9,8 @@ Tolerances (fixed before the first run):
     the exact one; plus one bf16 step where it is rounded to bf16.  fp32 weight
     gradients are summed in segments of 4096 rows.
 """
+import math
+
 import pytest
 import torch
 
@@ -351,6 +353,29 @@ def test_python_layer_refusals(sw):
     square = _ints(g, 20, 32)
     with pytest.raises(sw.SwigluError, match="ALIAS"):
         sw.swiglu_grouped_mm_fwd(square, _ints(g, 2, 32, 32), ends, y=square)
+
+
+@pytest.mark.parametrize("N,K", [(264, 520), (72, 64), (1032, 1288)])
+def test_weight_gradient_of_every_remainder(sw, N, K):
+    """Groups of 0 to 130 rows, in both orders: every number of rows in a group's last
+    block, next to a group of NaN, and at the end of the tensor."""
+    for counts in (list(range(131)), list(range(130, -1, -1))):
+        bad = counts.index(61)
+        rows, g = sum(counts), _gen(N + counts[0])
+        x, dy = _ints(g, rows, K), _ints(g, rows, N)
+        first = sum(counts[:bad])
+        x[first:first + 61], dy[first:first + 61] = math.nan, math.nan
+        for dtype in (torch.bfloat16, torch.float32):
+            dw = sw.swiglu_grouped_mm_wgrad(dy, x, _ends(counts), dtype=dtype)
+            r0 = 0
+            for e, c in enumerate(counts):
+                ref = (dy[r0:r0 + c].double().T @ x[r0:r0 + c].double()).to(dtype)
+                r0 += c
+                if e == bad:
+                    assert bool(dw[e].isnan().all())
+                else:
+                    assert torch.equal(dw[e], ref), f"group of {c} rows, {dtype}"
+    assert sw.grouped_timeout_flag() == 0
 
 
 def test_many_groups(sw):
