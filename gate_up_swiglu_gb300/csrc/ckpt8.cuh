@@ -234,9 +234,9 @@ __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
 // GB/s copy: packs of 8 bytes bf16 [8192, 2 x 5460] 66 us (0.82) and 62 us (0.87),
 // fp32 [8192, 2 x 2730] 61 us (0.77) and 57 us (0.83); of 4 bytes [8192, 2 x 10922]
 // 164 us (0.66) and 147 us (0.73); elements bf16 [8192, 2 x 5503] 126 us (0.43) and
-// 108 us (0.50), fp32 [3000, 2 x 5503] 51.6 us (0.67) and 50.8 us (0.68).  The fewer
-// bytes a memory instruction moves the more it is these that bound them: taking
-// arithmetic out of the single elements gained 1 %.
+// 108 us (0.50), fp32 [3000, 2 x 5503] 51.6 us (0.67) and 50.8 us (0.68).  Packs
+// of 4 bytes keep the issue slots 76 - 78 % busy; single elements are bound by their
+// memory instructions (taking arithmetic out of them gained 1 %).
 
 template <typename E, int VEC>
 constexpr bool kNarrow = E::kBytes * VEC <= 8;

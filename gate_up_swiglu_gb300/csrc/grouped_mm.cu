@@ -314,7 +314,7 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int m, int 
 
 // Warps: 0 loads, 1 MMA, 2 .. epilogue, then the scheduler.  The epilogue has two warps per quarter of the accumulator's
 // lanes, which take every other chunk of columns each (with one the tile of a
-// short contraction took 4.3 instead of 3.7 us, kFc1 5.6 instead of 4.9).
+// short contraction took 3.1 instead of 2.2 us, kFc1 5.4 instead of 3.5).
 constexpr int kEpi = 8;
 constexpr int kScheduler = 2 + kEpi;
 constexpr int kPairThreads = 32 * (3 + kEpi);
@@ -624,8 +624,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 ++lt;
                 tc_fence_after();
                 const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
-                // (reading the next 32 columns ahead of storing these was no faster:
-                // 4.7 us per 256 x 256 tile of one contraction block against 4.3)
                 if (kChunk * set >= width) {  // no columns for this warp
                     if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
                     continue;
@@ -1215,9 +1213,11 @@ bool map3(EncodeTiled enc, CUtensorMap *map, const void *p, int64_t inner, int64
 }
 
 // The result: boxes of 64 bytes by 32 rows with the 64-byte swizzle, one warp's
-// part.  (Rows of 128 bytes, put together by two warps, took 4.0 - 4.3 us per
-// 256 x 256 tile against 3.7: the warps' meeting costs more than the wider rows
-// save.  Plain 32-byte stores from the accumulator's lanes took 5.4.)
+// part: 2.2 us per 256 x 256 tile of one contraction block, 4.5 TB/s.  (Rows of 128
+// bytes, put together by two warps, cost more in the warps' meeting than the wider
+// rows save, 4.0 - 4.3 against 3.7 us at the time; plain 32-byte stores from the
+// accumulator's lanes took 5.4.  A second buffer per warp, and the two halves of a
+// row's 128 bytes stored by one warp in turn, were no faster.)
 bool out_map(EncodeTiled enc, CUtensorMap *map, void *p, int eb, int64_t inner, int64_t rows, int64_t outer) {
     const cuuint64_t d[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
     const cuuint64_t st[2] = {(cuuint64_t)(inner * eb), (cuuint64_t)(inner * rows * eb)};
