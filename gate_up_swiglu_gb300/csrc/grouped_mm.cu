@@ -965,7 +965,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
         const int box_cols = (width + 63) / 64;  // kWgrad
         const uint32_t bytes =
             (uint32_t)(A_BYTES + (MODE == kWgrad ? box_cols * (A_BYTES / 2) : width * BK * 2));
-        for (int kb = kb0, it = 0; kb < kb1 && !*abort_flag; ++kb, ++it) {
+        int it = 0;
+        for (int kb = kb0; kb < kb1 && !*abort_flag; ++kb, ++it) {
             const int s = it % kStages;
             if (!mbar_wait(empty0 + 8 * s, ((it / kStages) & 1) ^ 1)) {
                 *abort_flag = 1;
@@ -993,6 +994,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
                 continue;
             }
             tma_load_2d(sa + A_BYTES, &p.b[width / 16 - 1], bar, kb * BK, t.r0 + t.n0);
+        }
+        // every load has landed before this CTA can leave, also when a wait ran out
+        for (int k = it > kStages ? it - kStages : 0; k < it; ++k) {
+            if (last_rows != 0 && k == kb1 - 1 - kb0)
+                mbar_wait(landed, 0);
+            else
+                mbar_wait(full0 + 8 * (k % kStages), (k / kStages) & 1);
         }
     } else if (warp == 1 && kb1 > kb0 && elect_one()) {
         const uint32_t idesc = instr_desc(kAMn, kBMn, 128, width);
