@@ -253,17 +253,18 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Groups &g, int t)
 
 __device__ __forceinline__ float4 lds128(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// y for 8 gates and ups of one row, from fp32, rounded once: the operations of
+// y for N gates and ups of one row, from fp32, rounded once: the operations of
 // the streaming kernels (swiglu::activation), with the row weight last.  Without a
 // gate below -64 two elements go through each multiplication and addition (each
 // lane rounded as the scalar operation rounds).
-__device__ __forceinline__ void activate8(const float (&g)[8], const float (&u)[8], float w, uint32_t (&out)[4]) {
+template <int N>
+__device__ __forceinline__ void activate(const float (&g)[N], const float (&u)[N], float w, uint32_t (&out)[N / 2]) {
     float gmin = g[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) gmin = fminf(gmin, g[i]);
+    for (int i = 1; i < N; ++i) gmin = fminf(gmin, g[i]);
     if (gmin < -64.0f) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
+        for (int i = 0; i < N; i += 2) {
             float r[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -276,7 +277,7 @@ __device__ __forceinline__ void activate8(const float (&g)[8], const float (&u)[
         using namespace swiglu;
         const uint64_t neg_log2e = x2(-kLog2e, -kLog2e), one = x2(1.0f, 1.0f), w2 = x2(w, w);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
+        for (int i = 0; i < N; i += 2) {
             const uint64_t g2 = x2(g[i], g[i + 1]), u2 = x2(u[i], u[i + 1]);
             float t0, t1, d0, d1, r0, r1;
             x2_split(mul_x2(g2, neg_log2e), t0, t1);
@@ -707,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                 store16(fr + n, o[0], o[1], o[2], o[3]);
                             }
                             const float w = p.probs != nullptr && t.group != p.groups ? p.probs[row] : 1.0f;
-                            activate8(g, u, w, o);
+                            activate(g, u, w, o);
                             store16(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, o[0], o[1], o[2], o[3]);
                         }
                     } else if constexpr (MODE == kWgrad) {
@@ -847,6 +848,12 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float4 ld_own(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t n;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
@@ -858,42 +865,129 @@ __device__ __forceinline__ int slice_begin(int blocks, uint32_t s, uint32_t size
     return (int)(((uint64_t)(uint32_t)blocks * s) >> (31 - __clz((int)size)));
 }
 
-// R rows of four features summed over up to SL slices in rank order, every load
-// issued before the first is used (a load from another SM takes long).  `from`:
-// this CTA's address of the first row's features (the ups of kFc1 32 lanes on);
-// `step`: rows from one to the next; `rows`: how many there are; bit s of `have`:
-// slice s has a part.
+// Rows rank, rank + S, ... of a tile: their slices' sums added up in rank order and
+// stored.  A thread takes four features of every kPass-th of these rows, R rows at a
+// time, everything they need loaded before the first is used (a load from another
+// SM, a row's weight or dW's old value takes long, and a CTA has six warps).  `ring`:
+// this CTA's partial sums; bit s of `have`: slice s has a part.
 template <int MODE, int R, int SL>
-__device__ __forceinline__ void join_rows(uint32_t from, int step, int rows, uint32_t have, float (&g)[R][4],
-                                          float (&u)[R][4]) {
-    float4 a[R][SL], b[R][SL];
-#pragma unroll
-    for (int s = 0; s < SL; ++s) {
-        if (!(have >> s & 1)) continue;
-        const uint32_t at = map_to_rank(from, (uint32_t)s);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (i < rows) {
-                a[i][s] = ld_cluster(at + (uint32_t)(i * step * kPartialRow) * 4);
-                if (MODE == kFc1) b[i][s] = ld_cluster(at + (uint32_t)(i * step * kPartialRow + 32) * 4);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) g[i][x] = u[i][x] = 0.0f;
+__device__ __forceinline__ void join_rows(const Params &p, const Tile &t, uint32_t ring, int rank, int size,
+                                          uint32_t have) {
+    using St8 = swiglu::St<8, swiglu::kStStream>;
+    constexpr int kRowThreads = kSplitF<MODE> / 4;
+    constexpr int kPass = kSplitThreads / kRowThreads;  // rows of the CTA per pass
+    static_assert(kSplitThreads % kRowThreads == 0, "whole rows of threads");
+    const int f = (int)threadIdx.x % kRowThreads, col = t.m0 + 4 * f, n = p.features;
+    const int step = kPass * size, first = rank + (int)threadIdx.x / kRowThreads * size;
+    // this thread's rows, and the turns of all (the same for a whole warp: the block
+    // maximum is shuffled)
+    int left = col < n && first < t.cnt ? (t.cnt - first + step - 1) / step : 0;
+    const int turns = rank < t.cnt ? (t.cnt - rank + step * R - 1) / (step * R) : 0;
+    // kFc1: 32 gates, 32 ups, 32 gates, 32 ups
+    uint32_t from = ring + (uint32_t)(first * kPartialRow + (MODE == kFc1 ? f / 8 * 64 + f % 8 * 4 : f * 4)) * 4;
+    int64_t row = (int64_t)t.r0 + t.n0 + first;
+    // the M side of kWgrad are dW's columns, the N side its rows
+    const int eb = MODE == kWgrad && p.f32_out ? 4 : 2;
+    char *out = static_cast<char *>(p.out) +
+                ((MODE == kWgrad ? (int64_t)t.group * p.cols + t.n0 + first : row) * n + col) * eb;
+    const int64_t out_step = (int64_t)step * n * eb;
+    const auto pack = [](const float (&v)[4], uint32_t (&w)[2]) {
+        swiglu::BF16::put2(w, 0, v[0], v[1]);
+        swiglu::BF16::put2(w, 2, v[2], v[3]);
+    };
+#pragma unroll 1
+    for (int turn = 0; turn < turns; ++turn) {
+        float4 a[R][SL], b[R][SL], old[R];
+        float wr[R];
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
-            if (i < rows && (have >> s & 1)) {
-                g[i][0] = __fadd_rn(g[i][0], a[i][s].x), g[i][1] = __fadd_rn(g[i][1], a[i][s].y);
-                g[i][2] = __fadd_rn(g[i][2], a[i][s].z), g[i][3] = __fadd_rn(g[i][3], a[i][s].w);
-                if (MODE == kFc1) {
-                    u[i][0] = __fadd_rn(u[i][0], b[i][s].x), u[i][1] = __fadd_rn(u[i][1], b[i][s].y);
-                    u[i][2] = __fadd_rn(u[i][2], b[i][s].z), u[i][3] = __fadd_rn(u[i][3], b[i][s].w);
+            if (!(have >> s & 1)) continue;
+            const uint32_t at = SL == 1 ? from : map_to_rank(from, (uint32_t)s);
+            const auto load = [&](uint32_t offset) { return SL == 1 ? ld_own(at + offset) : ld_cluster(at + offset); };
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                if (i < left) {
+                    a[i][s] = load((uint32_t)(i * step * kPartialRow) * 4);
+                    if (MODE == kFc1) b[i][s] = load((uint32_t)(i * step * kPartialRow + 32) * 4);
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            wr[i] = 1.0f;
+            if (MODE == kFc1 && i < left && p.probs != nullptr && t.group != p.groups) wr[i] = p.probs[row + i * step];
+            if (MODE == kWgrad && i < left && p.accumulate)
+                old[i] = *reinterpret_cast<const float4 *>(out + i * out_step);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const bool in = i < left;
+            float g[4] = {}, u[4] = {};
+#pragma unroll
+            for (int s = 0; s < SL; ++s) {
+                if (in && (have >> s & 1)) {
+                    g[0] = __fadd_rn(g[0], a[i][s].x), g[1] = __fadd_rn(g[1], a[i][s].y);
+                    g[2] = __fadd_rn(g[2], a[i][s].z), g[3] = __fadd_rn(g[3], a[i][s].w);
+                    if (MODE == kFc1) {
+                        u[0] = __fadd_rn(u[0], b[i][s].x), u[1] = __fadd_rn(u[1], b[i][s].y);
+                        u[2] = __fadd_rn(u[2], b[i][s].z), u[3] = __fadd_rn(u[3], b[i][s].w);
+                    }
+                }
+            }
+            uint32_t w[2];
+            if constexpr (MODE == kFc1) {
+                if (p.q != nullptr) {
+                    float mg = ckpt8::finite_amax<4>(g), mu = ckpt8::finite_amax<4>(u);
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) {  // eight threads hold a block
+                        mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+                        mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+                    }
+                    if (in) {
+                        const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
+                        uint32_t qg, qu;
+                        ckpt8::encode<4>(g, ckpt8::encode_factor(cg), &qg);
+                        ckpt8::encode<4>(u, ckpt8::encode_factor(cu), &qu);
+                        uint8_t *qr = p.q + row * 2 * n + col;
+                        swiglu::St<4, swiglu::kStStream>::run(qr, &qg);
+                        swiglu::St<4, swiglu::kStStream>::run(qr + n, &qu);
+                        if (f % 8 == 0) {
+                            const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
+                            uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
+                            sr[0] = (uint8_t)cg;
+                            sr[nb] = (uint8_t)cu;
+                        }
+                    }
+                }
+                if (in) {
+                    if (p.fc1 != nullptr) {
+                        __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
+                        pack(g, w);
+                        St8::run(fr, w);
+                        pack(u, w);
+                        St8::run(fr + n, w);
+                    }
+                    activate(g, u, wr[i], w);
+                    St8::run(out, w);
+                }
+            } else if (in) {
+                if (MODE == kWgrad && p.f32_out) {
+                    if (p.accumulate) {
+                        g[0] = __fadd_rn(old[i].x, g[0]), g[1] = __fadd_rn(old[i].y, g[1]);
+                        g[2] = __fadd_rn(old[i].z, g[2]), g[3] = __fadd_rn(old[i].w, g[3]);
+                    }
+                    store16(out, __float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
+                            __float_as_uint(g[3]));
+                } else {
+                    pack(g, w);
+                    St8::run(out, w);
+                }
+            }
+            row += step;
+            out += out_step;
+        }
+        left -= R;
+        from += (uint32_t)(R * step * kPartialRow) * 4;
     }
 }
 
@@ -1059,119 +1153,18 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
     __syncthreads();
     if (size > 1) cluster_sync();
     if (live) {
-        // rows rank, rank + S, ... of the tile: 16 (kFc1) or 32 threads a row, four
-        // features each; a few rows at once of up to two slices, or one of up to eight
-        constexpr int kRowThreads = kSplitF<MODE> / 4;
-        constexpr int kPass = kSplitThreads / kRowThreads;  // rows of the CTA per pass
-        static_assert(kSplitThreads % kRowThreads == 0, "whole rows of threads");
         uint32_t have = 0;  // slices with a block (a short group of kWgrad leaves some without)
         if (t.group != p.groups) {
             const int blocks = ((MODE == kWgrad ? t.rows : p.depth) + BK - 1) / BK;
             for (uint32_t s = 0; s < size; ++s)
                 if (slice_begin(blocks, s, size) < slice_begin(blocks, s + 1, size)) have |= 1u << s;
         }
-        const int f = (int)threadIdx.x % kRowThreads;
-        // kFc1: 32 gates, 32 ups, 32 gates, 32 ups
-        const int lane0 = MODE == kFc1 ? f / 8 * 64 + f % 8 * 4 : f * 4;
-        const int col = t.m0 + 4 * f;
-        const int step = kPass * (int)size;
-        constexpr int kRows = MODE == kFc1 ? 2 : 4;
-        const int at_once = size <= 2 ? kRows : 1;
-        // (the trip counts are the same for a whole warp: the block maximum is shuffled)
-        for (int r0 = (int)rank; r0 < t.cnt; r0 += at_once * step) {
-            const int first = r0 + (int)(threadIdx.x / kRowThreads) * (int)size;
-            const int rows = col < p.features && first < t.cnt ? (t.cnt - first + step - 1) / step : 0;
-            const uint32_t from = ring + (uint32_t)(first * kPartialRow + lane0) * 4;
-            float gs[kRows][4], us[kRows][4];
-            if (size <= 2) {
-                join_rows<MODE, kRows, 2>(from, step, rows, have, gs, us);
-            } else {
-                float g1[1][4], u1[1][4];
-                join_rows<MODE, 1, 8>(from, step, rows, have, g1, u1);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) gs[0][x] = g1[0][x], us[0][x] = u1[0][x];
-            }
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                if (i >= at_once || r0 + i * step >= t.cnt) break;
-                const int r = first + i * step;
-                const bool in = r < t.cnt && col < p.features;
-                float(&g)[4] = gs[i];
-                float(&u)[4] = us[i];
-                const int64_t row = (int64_t)t.r0 + t.n0 + r;
-                const auto pack = [](const float (&v)[4], uint32_t (&w)[2]) {
-                    swiglu::BF16::put2(w, 0, v[0], v[1]);
-                    swiglu::BF16::put2(w, 2, v[2], v[3]);
-                };
-                using St8 = swiglu::St<8, swiglu::kStStream>;
-                if constexpr (MODE == kFc1) {
-                    const int n = p.features;
-                    if (p.q != nullptr) {
-                        float mg = ckpt8::finite_amax<4>(g), mu = ckpt8::finite_amax<4>(u);
-#pragma unroll
-                        for (int o = 1; o < 8; o <<= 1) {  // eight threads hold a block
-                            mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-                            mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
-                        }
-                        if (in) {
-                            const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
-                            uint32_t qg, qu;
-                            ckpt8::encode<4>(g, ckpt8::encode_factor(cg), &qg);
-                            ckpt8::encode<4>(u, ckpt8::encode_factor(cu), &qu);
-                            uint8_t *qr = p.q + row * 2 * n + col;
-                            swiglu::St<4, swiglu::kStStream>::run(qr, &qg);
-                            swiglu::St<4, swiglu::kStStream>::run(qr + n, &qu);
-                            if (f % 8 == 0) {
-                                const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
-                                uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
-                                sr[0] = (uint8_t)cg;
-                                sr[nb] = (uint8_t)cu;
-                            }
-                        }
-                    }
-                    if (in) {
-                        uint32_t w[2];
-                        if (p.fc1 != nullptr) {
-                            __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
-                            pack(g, w);
-                            St8::run(fr, w);
-                            pack(u, w);
-                            St8::run(fr + n, w);
-                        }
-                        const float wr = p.probs != nullptr && t.group != p.groups ? p.probs[row] : 1.0f;
-                        float y[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const swiglu::Act act = swiglu::activation<swiglu::BF16, false, true>(g[i]);
-                            y[i] = __fmul_rn(__fmul_rn(__fmul_rn(act.silu, u[i]), wr), act.scale);
-                        }
-                        pack(y, w);
-                        St8::run(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, w);
-                    }
-                } else if (MODE == kWgrad && in) {
-                    // the M side are dW's columns, the N side its rows
-                    const int64_t at = ((int64_t)t.group * p.cols + t.n0 + r) * p.features + col;
-                    if (p.f32_out) {
-                        float *o = static_cast<float *>(p.out) + at;
-                        if (p.accumulate) {
-                            const float4 old = *reinterpret_cast<const float4 *>(o);
-                            g[0] = __fadd_rn(old.x, g[0]), g[1] = __fadd_rn(old.y, g[1]);
-                            g[2] = __fadd_rn(old.z, g[2]), g[3] = __fadd_rn(old.w, g[3]);
-                        }
-                        store16(o, __float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
-                                __float_as_uint(g[3]));
-                    } else {
-                        uint32_t w[2];
-                        pack(g, w);
-                        St8::run(static_cast<__nv_bfloat16 *>(p.out) + at, w);
-                    }
-                } else if (in) {
-                    uint32_t w[2];
-                    pack(g, w);
-                    St8::run(static_cast<__nv_bfloat16 *>(p.out) + row * p.features + col, w);
-                }
-            }
-        }
+        if (size == 1)
+            join_rows<MODE, 4, 1>(p, t, ring, (int)rank, (int)size, have);
+        else if (size == 2)
+            join_rows<MODE, MODE == kFc1 ? 2 : 4, 2>(p, t, ring, (int)rank, (int)size, have);
+        else
+            join_rows<MODE, 1, 8>(p, t, ring, (int)rank, (int)size, have);
     }
     __syncwarp();
     if (size > 1) cluster_sync_read();  // no CTA leaves while another may still read its sums
