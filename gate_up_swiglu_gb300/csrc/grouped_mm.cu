@@ -1159,10 +1159,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
             for (uint32_t s = 0; s < size; ++s)
                 if (slice_begin(blocks, s, size) < slice_begin(blocks, s + 1, size)) have |= 1u << s;
         }
+        // (more rows at once are slower: the code that is fetched for them costs more
+        // than the latency that they hide, 6.7 against 6.3 us for 128 rows in 2 slices)
         if (size == 1)
             join_rows<MODE, 4, 1>(p, t, ring, (int)rank, (int)size, have);
         else if (size == 2)
             join_rows<MODE, MODE == kFc1 ? 2 : 4, 2>(p, t, ring, (int)rank, (int)size, have);
+        else if (size == 4)
+            join_rows<MODE, MODE == kFc1 ? 1 : 2, 4>(p, t, ring, (int)rank, (int)size, have);
         else
             join_rows<MODE, 1, 8>(p, t, ring, (int)rank, (int)size, have);
     }
@@ -1290,33 +1294,35 @@ swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_st
 // Pairs or split?  The rule estimates both times in nanoseconds from the tiles of
 // groups of equal size, which is all the host knows: operand bytes per SM at the
 // rates the two kernels reach, times the rounds of the grid, plus what a launch,
-// a tile and the joining of the sums take.  The constants are a fit to the times
-// of all five choices on 14,000 shapes (forward, fc1 and both gradients; 1 to
-// 32768 rows, 1 to 64 groups, widths 64 to 14336); with them the choice is on
-// average 2.3 % slower than the best one, where always pairs are 20 % and always
-// one CTA per tile 47 % slower.
+// a tile, the joining of the sums and the CTAs beyond the last tile take.  The
+// constants are a fit to the times of all five choices on 14,500 shapes (forward,
+// fc1 and both gradients; 1 to 32768 rows, 1 to 64 groups, widths 64 to 14336); with
+// them the choice is on average 2.4 % slower than the best one, where always pairs
+// are 22 % and always one CTA per tile 36 % slower.
 struct Plan {
     int size;  // CTAs per tile of the split kernel; 0: pairs
 };
 
 // `same` groups of `rows_per` rows (kWgrad: of dW's columns) by `features`; pair_f
-// and split_f: features of a tile, nt: rows of a tile of the split kernel;
-// least_size: the fewest slices a sum may be cut into (pairs cut it themselves).
-Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int split_f, int nt, int64_t kblocks,
-          int64_t least_size = 1) {
+// and split_f: features of a tile, nt: rows of a tile of the split kernel, most: its
+// tiles at most; least_size: the fewest slices a sum may be cut into (pairs cut it
+// themselves).
+Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int split_f, int nt, int64_t most,
+          int64_t kblocks, int64_t least_size = 1) {
     const int64_t pair_n = rows_per < TILE_N ? ceil_div(rows_per, 32) * 32 : TILE_N;
     const int64_t pair_tiles = same * ceil_div(rows_per, TILE_N) * ceil_div(features, pair_f);
-    const int64_t pair_depth = kblocks * (A_BYTES + pair_n * BK) / 112;
+    const int64_t pair_depth = kblocks * (A_BYTES + pair_n * BK) * 100 / 8955;
     Plan best = {0};
-    int64_t least = ceil_div(pair_tiles, kSms / 2) * (pair_depth > 1000 ? pair_depth : 1000) + 5920;
+    int64_t least = ceil_div(pair_tiles, kSms / 2) * (pair_depth > 1530 ? pair_depth : 1530) + 8270;
     const int64_t split_n = rows_per < nt ? ceil_div(rows_per, 16) * 16 : nt;
     const int64_t split_tiles = same * ceil_div(rows_per, nt) * ceil_div(features, split_f);
+    const int64_t beyond = most > split_tiles ? most - split_tiles : 0;
     for (int size = 1; size <= 8 && (size == 1 || 2 * size <= kblocks); size *= 2) {
         if (size < least_size) continue;
         const int64_t ctas = split_tiles * size;
         const int64_t bytes = ceil_div(kblocks, size) * (A_BYTES + split_n * BK * 2);
-        const int64_t time = (ctas <= kSms ? bytes / 96 : ceil_div(ctas, kSms) * bytes / 111) +
-                             ceil_div(ctas, 2 * kSms) * (3850 + 69 * split_n / size) + (size > 1 ? 1250 : 0);
+        const int64_t time = (ctas <= kSms ? bytes * 10 / 896 : ceil_div(ctas, kSms) * bytes * 10 / 1066) +
+                             ceil_div(ctas, 2 * kSms) * 6810 + (size > 1 ? 870 : 0) + beyond * size * 17;
         if (time < least) {
             least = time;
             best.size = size;
@@ -1332,9 +1338,9 @@ swiglu_status_t launch_rows(const Params &p, swiglu_stream_t stream) {
     if (pairs > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
     const bool few = p.rows <= 32;
     const int64_t same = p.rows < p.groups ? p.rows : p.groups;
-    const Plan pl = plan(same, ceil_div(p.rows, same), p.features, kTileF<MODE>, kSplitF<MODE>, few ? 32 : 128,
-                         ceil_div(p.depth, BK));
     const int64_t tiles = most_tiles(p.rows, p.groups, p.features, kSplitF<MODE>, few ? 32 : 128);
+    const Plan pl = plan(same, ceil_div(p.rows, same), p.features, kTileF<MODE>, kSplitF<MODE>, few ? 32 : 128, tiles,
+                         ceil_div(p.depth, BK));
     if (pl.size == 0 || tiles > INT32_MAX / 16) return launch_pairs<MODE>(p, pairs, stream);
     return few ? launch_split<MODE, 32>(p, tiles, pl.size, stream) : launch_split<MODE, 128>(p, tiles, pl.size, stream);
 }
@@ -1504,14 +1510,15 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     p.accumulate = accumulate != 0;
     // Pairs: M is dW's rows, N its columns.  Split: the other way round, so that the
     // lanes run along dW's rows; an fp32 sum's slices stay within a segment.
-    const Plan pl = plan(groups, N, K, 256, kSplitF<kWgrad>, 128, ceil_div(ceil_div(rows, groups), BK),
+    const int64_t split_tiles = groups * ceil_div(N, 128) * ceil_div(K, kSplitF<kWgrad>);
+    const Plan pl = plan(groups, N, K, 256, kSplitF<kWgrad>, 128, split_tiles, ceil_div(ceil_div(rows, groups), BK),
                          p.f32_out ? ceil_div(rows, kSegmentRows) : 1);
     if (pl.size > 0) {
         if (!map2(enc, &p.a, x, K, rows, BK) || !map2(enc, &p.b[0], dy, N, rows, BK))
             return moe::cuda_fail(cudaErrorInvalidValue);
         p.features = (int)K;
         p.cols = (int)N;
-        return launch_split<kWgrad, 128>(p, groups * ceil_div(N, 128) * ceil_div(K, kSplitF<kWgrad>), pl.size, stream);
+        return launch_split<kWgrad, 128>(p, split_tiles, pl.size, stream);
     }
     if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK) ||
         !out_map(enc, &p.c, dw, eb, K, N, groups))
