@@ -126,9 +126,9 @@ __device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t *q) {
 // writes y, two codes and 2/32 scale bytes; the backward reads dy, the codes
 // and scales and writes dx (and y).  In bf16 that is 8.06 bytes a pair either
 // way for about 15 (forward) and 20 (backward) instructions, so both are bound
-// by HBM: [8192, 2 x 14336] bf16 forward 150 us (0.95 of the 6680 GB/s copy),
-// backward without weights 140 us (1.01; 169 us with y, 1.05), fp32
-// [8192, 2 x 4096] 72 / 71 us (0.98 / 0.99).
+// by HBM: [8192, 2 x 14336] bf16 forward 136 us (1.04 of the 6680 GB/s copy),
+// backward without weights 140 us (1.01; 169 us with y, 1.04), fp32
+// [8192, 2 x 4096] 69 / 71 us (1.02 / 0.99).
 //
 // A pack is VEC elements of one half; a block of 32 columns is 32 / VEC
 // neighbouring lanes, so the forward's block maximum is a shuffle inside that
@@ -152,8 +152,8 @@ struct FwdParams {
 };
 
 // U packs per thread, T packs apart, all loaded first: 1 for 32-byte packs (two:
-// 172 us against 150 for [8192, 2 x 14336] bf16), 2 for 16-byte packs (one: 186 us
-// against 175 for [8192, 2 x 14344]).  CTAs of 256 or 64 threads were no faster.
+// 140 us against 136 for [8192, 2 x 14336] bf16), 2 for 16-byte packs (one: 164 us
+// against 153 for [8192, 2 x 14344]).  CTAs of 256 or 64 threads were no faster.
 template <typename E, int VEC, int U, int T>
 __global__ void __launch_bounds__(T) ckpt8_fwd_kernel(const FwdParams p) {
     swiglu::await_previous_grid();
