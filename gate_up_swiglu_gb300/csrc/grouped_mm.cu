@@ -661,7 +661,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 ++lt;
                 tc_fence_after();
                 const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
-                if (kChunk * set >= width) {  // no columns for this warp
+                // no columns for this warp, or a group without rows whose dW is added to:
+                // it stays as it is (adding zeros would turn -0 into 0 and rewrite NaNs)
+                if (kChunk * set >= width || (MODE == kWgrad && p.accumulate && kblocks == 0)) {
                     if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
                     continue;
                 }
@@ -1197,7 +1199,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
         }
         // (more rows at once are slower: the code that is fetched for them costs more
         // than the latency that they hide, 6.7 against 6.3 us for 128 rows in 2 slices)
-        if (size == 1)
+        if (MODE == kWgrad && p.accumulate && have == 0) {
+            // nothing to add: dW stays as it is
+        } else if (size == 1)
             join_rows<MODE, 4, 1>(p, t, ring, (int)rank, (int)size, have);
         else if (size == 2)
             join_rows<MODE, MODE == kFc1 ? 2 : 4, 2>(p, t, ring, (int)rank, (int)size, have);

@@ -438,3 +438,28 @@ def test_large_offsets(sw):
     assert _same_bits(y[pick] + 0.0, ref.bfloat16() + 0.0)
     ref = torch.einsum("rn,rnk->rk", y[pick].double(), w[which].double()) * live
     assert _same_bits(dx[pick] + 0.0, ref.bfloat16() + 0.0)
+
+
+@pytest.mark.parametrize("N,K,scale", [(136, 72, 1), (1032, 1288, 8)])
+@pytest.mark.parametrize("some", [True, False])
+def test_accumulating_leaves_empty_groups_as_they_are(sw, N, K, scale, some):
+    """dW of a group without rows keeps its bits: -0, subnormals, infinities and NaNs
+    with a payload among them; next to it the sum is added, subnormals kept.  The
+    wider product is the CTA pairs', the other one is split."""
+    g = _gen(13)
+    counts = [0, 40 * scale, 0, 9 * scale, 0] if some else [0] * 5
+    rows, E, ends = sum(counts) + 7, 5, _ends(counts)
+    x, dy = _ints(g, rows, K), torch.zeros(rows, N, device="cuda").bfloat16()
+    dy[:, ::3] = _ints(g, rows, N)[:, ::3]
+    odd = torch.tensor([-2 ** 31, 1, 0x7fffff, 0x7fc01234, 0x7f800000, 0x3f800000, 5 - 2 ** 31, -0x345678],
+                       dtype=torch.int32, device="cuda")
+    start = odd.repeat(E * N * K // 8).view(E, N, K)
+    dw = sw.swiglu_grouped_mm_wgrad(dy, x, ends, dw=start.clone().view(torch.float32), accumulate=True)
+    ref, _ = R.wgrad(dy, x, ends, E)
+    want = start.view(torch.float32) + ref.float()
+    for e, c in enumerate(counts):
+        if c == 0:
+            assert torch.equal(dw[e].view(torch.int32), start[e])
+        else:  # (the sums are integers, exact; a NaN need not keep its payload)
+            same = (dw[e] == want[e]) | (dw[e].isnan() & want[e].isnan())
+            assert bool(same.all())
