@@ -62,3 +62,11 @@ def test_counts_of_two_dimensions_are_refused(mods):
     for shape in ((1, 4), (4, 1), (2, 2)):
         with pytest.raises(ValueError, match="rows of each expert"):
             m(torch.zeros(4, 16).bfloat16(), torch.tensor([1, 2, 1, 0]).view(shape))
+
+
+def test_counts_of_two_dimensions_are_summed_over_all(mods):
+    """Not along the first one only, which leaves [[3, 0, 5]] as it is."""
+    _, ex = mods
+    for shape in ((1, 3), (3, 1), (3,)):
+        ends = ex.group_ends(torch.tensor([3, 0, 5]).view(shape))
+        assert ends.dtype == torch.int32 and ends.tolist() == [3, 3, 8]
