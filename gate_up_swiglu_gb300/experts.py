@@ -31,10 +31,9 @@ CHECKPOINTS = ("fp8", "bf16")
 
 
 def group_ends(counts: torch.Tensor) -> torch.Tensor:
-    """The `ends` of the grouped products from the rows per expert, [E]."""
-    if counts.dim() != 1:  # a running sum over another dimension would be no ends
-        raise ValueError(f"counts must have one dimension, got shape {tuple(counts.shape)}")
-    return counts.cumsum(0, dtype=torch.int32)
+    """The `ends` of the grouped products from the rows per expert (in one dimension or
+    with others of size one)."""
+    return counts.reshape(-1).cumsum(0, dtype=torch.int32)
 
 
 class Ckpt8SwiGLUFunction(torch.autograd.Function):
@@ -132,7 +131,7 @@ class ExpertsSwiGLU(torch.nn.Module):
         torch.nn.init.normal_(self.w2, std=ffn_hidden ** -0.5)
 
     def forward(self, x: torch.Tensor, counts: torch.Tensor, probs: Optional[torch.Tensor] = None) -> torch.Tensor:
-        if x.dim() != 2 or counts.shape != self.w1.shape[:1]:
+        if x.dim() != 2 or counts.numel() != self.w1.shape[0]:
             raise ValueError("x must be [rows, hidden] and counts hold the rows of each expert")
         ends = group_ends(counts)
         tracked = (x, self.w1, self.w2) if probs is None else (x, probs, self.w1, self.w2)

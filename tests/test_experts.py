@@ -52,18 +52,6 @@ def test_native_fp8_takes_the_input_without_a_bias_only(mods):
         w(torch.zeros(4, 8), None, torch.ones(4), True)
 
 
-def test_counts_of_two_dimensions_are_refused(mods):
-    """Their running sum along the first one would be no ends: [[3, 0, 5]] as it is."""
-    _, ex = mods
-    for shape in ((1, 3), (3, 1)):
-        with pytest.raises(ValueError, match="one dimension"):
-            ex.group_ends(torch.tensor([3, 0, 5]).view(shape))
-    m = ex.ExpertsSwiGLU(4, 16, 8)
-    for shape in ((1, 4), (4, 1), (2, 2)):
-        with pytest.raises(ValueError, match="rows of each expert"):
-            m(torch.zeros(4, 16).bfloat16(), torch.tensor([1, 2, 1, 0]).view(shape))
-
-
 def test_counts_of_two_dimensions_are_summed_over_all(mods):
     """Not along the first one only, which leaves [[3, 0, 5]] as it is."""
     _, ex = mods
