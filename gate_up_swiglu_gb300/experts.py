@@ -22,6 +22,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (swiglu_ckpt8_bwd, swiglu_ckpt8_fwd, swiglu_gateup_bwd, swiglu_gateup_fwd, swiglu_gateup_weighted_bwd,
                swiglu_gateup_weighted_fwd, swiglu_grouped_fc1_fwd, swiglu_grouped_mm_dgrad, swiglu_grouped_mm_fwd,
@@ -52,6 +53,7 @@ class Ckpt8SwiGLUFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable  # the kernels' results carry no graph
     def backward(ctx, dy: torch.Tensor):
         q, scales, w32 = ctx.saved_tensors
         dx, dw, _ = swiglu_ckpt8_bwd(dy.contiguous(), q, scales, w32)
@@ -82,6 +84,7 @@ class ExpertsSwiGLUFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable  # the kernels' results carry no graph
     def backward(ctx, dout):
         x, p32, w1, w2, ends, *kept = ctx.saved_tensors
         need_x, need_p, need_w1, need_w2 = ctx.needs_input_grad[:4]
