@@ -878,17 +878,23 @@ static_assert(kSplitSmem<32> <= 113 * 1024 && kSplitSmem<128> <= 113 * 1024, "tw
 template <int MODE>
 constexpr int kSplitF = MODE == kFc1 ? 64 : 128;
 
+// Partial sums, which other threads and CTAs have written: neither load may be moved
+// over the barrier before it.
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr));
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
 __device__ __forceinline__ float4 ld_own(uint32_t addr) {
     float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 

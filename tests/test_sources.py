@@ -1,0 +1,32 @@
+"""Rules of the CUDA sources that no run shows reliably (no GPU)."""
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gate_up_swiglu_gb300", "csrc")
+
+
+def asm_statements(text):
+    """(line, statement) of every inline assembly statement."""
+    text = re.sub(r"//[^\n]*", "", text)
+    for m in re.finditer(r"\basm\b(\s+volatile)?\s*\(", text):
+        depth, at, quoted = 1, m.end(), False
+        while depth:
+            c = text[at]
+            if c == '"' and text[at - 1] != "\\":
+                quoted = not quoted
+            elif not quoted:
+                depth += (c == "(") - (c == ")")
+            at += 1
+        yield text.count("\n", 0, m.start()) + 1, text[m.start():at]
+
+
+@pytest.mark.parametrize("path", sorted(glob.glob(os.path.join(CSRC, "*.cu*"))), ids=os.path.basename)
+def test_shared_memory_loads_stay_behind_their_barriers(path):
+    """What another thread or CTA wrote to shared memory is read by assembly that the
+    compiler may neither drop, repeat nor move over a barrier."""
+    for line, s in asm_statements(open(path).read()):
+        if re.search(r"\bld\.shared\b", s):
+            assert re.match(r"asm\s+volatile", s) and '"memory"' in s, f"{os.path.basename(path)}:{line}"
