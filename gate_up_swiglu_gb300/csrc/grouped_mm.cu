@@ -483,10 +483,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int k = 0;; ++k) {
                 const int slot = k % kTileSlots;
                 if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) *abort_flag = 1;
-                if (k > 0 || tile >= tiles) tile = *abort_flag ? -1 : next();
                 Tile t;
                 t.group = -1;
-                if (tile >= 0 && !*abort_flag) t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
+                if (k > 0 || tile >= tiles) tile = *abort_flag ? -1 : next();
+                while (tile >= 0 && !*abort_flag) {
+                    t = tile_at<MODE, kTileF<MODE>, TILE_N, 32>(p, groups, tile);
+                    // a group without rows whose dW is added to: dW stays as it is (adding
+                    // zeros would turn -0 into 0 and rewrite NaNs)
+                    if (!(MODE == kWgrad && p.accumulate && t.rows == 0)) break;
+                    t.group = -1;
+                    tile = next();
+                }
                 publish(tile0 + 32 * slot, tile_full0 + 8 * slot, t);
                 if (t.group < 0) break;
             }
@@ -661,9 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 ++lt;
                 tc_fence_after();
                 const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
-                // no columns for this warp, or a group without rows whose dW is added to:
-                // it stays as it is (adding zeros would turn -0 into 0 and rewrite NaNs)
-                if (kChunk * set >= width || (MODE == kWgrad && p.accumulate && kblocks == 0)) {
+                if (kChunk * set >= width) {  // no columns for this warp
                     if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
                     continue;
                 }
