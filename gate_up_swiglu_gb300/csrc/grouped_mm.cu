@@ -104,6 +104,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return mbar_wait_or_flag<kCluster>(bar, parity, &g_timeout);
 }
 
+// A pair of which a wait ran out may leave loads of either CTA in flight that nobody
+// waits for (each counts on a barrier of the leader, whose phase the other CTA's part
+// may never complete), or an answer of the launch control.  So whoever gives up tells
+// both CTAs, and after their last meeting, when nothing more is issued, both keep their
+// shared memory for 10 ms, thousands of times what a load takes.
+constexpr unsigned long long kSettleNs = 10000000ull;
+
+__device__ __noinline__ void settle() {
+    const uint64_t t0 = now_ns();
+    while (now_ns() - t0 < kSettleNs) __nanosleep(1000);
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -426,6 +438,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const Groups groups = {starts, base};
     const int tiles = base[p.groups + 1];
 
+    // A wait of this thread ran out: both CTAs stop.  (The epilogue's warps set their own
+    // CTA's flag alone: its producer stops then, and the leader's MMA thread, left without
+    // operands, tells both.  Two instructions more in their loop cost 1 - 2 % of a call
+    // that writes mostly zeros.)
+    const auto give_up = [&]() {
+        *abort_flag = 1;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(st0 + OFF_ABORT, rank ^ 1u)), "r"(1)
+                     : "memory");
+    };
+
     // contraction blocks of a tile
     const auto blocks_of = [&](const Tile &t) {
         if (MODE == kWgrad) return (t.rows + BK - 1) / BK;
@@ -441,7 +463,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int slot = k % kTileSlots;
         Tile t;
         t.group = -1;
-        if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1)) t = read_tile(tile0 + 32 * slot);
+        if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1))
+            t = read_tile(tile0 + 32 * slot);
+        else
+            give_up();
         mbar_arrive_cluster_read(tile_empty_leader0 + 8 * slot);
         return t;
     };
@@ -468,11 +493,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 do {
                     mbar_arrive_expect_tx(clc_bar, 16);
                     clc_try_cancel(clc_resp, clc_bar);
-                    if (!mbar_wait<true>(clc_bar, asks++ & 1)) return -1;
+                    if (!mbar_wait<true>(clc_bar, asks++ & 1)) {
+                        give_up();
+                        return -1;
+                    }
                     const int x = clc_cancelled_cta(clc_resp);
                     if (x < 0) return -1;  // no pending cluster was left
                     if ((x & 1) != 0 || x >= (int)gridDim.x) {  // not a cluster's first CTA of this grid
-                        *abort_flag = 1;
+                        give_up();
                         atomicExch(&g_timeout, 1);
                         return -1;
                     }
@@ -482,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             };
             for (int k = 0;; ++k) {
                 const int slot = k % kTileSlots;
-                if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) *abort_flag = 1;
+                if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) give_up();
                 Tile t;
                 t.group = -1;
                 if (k > 0 || tile >= tiles) tile = *abort_flag ? -1 : next();
@@ -512,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int kb = 0; kb < kblocks && !*abort_flag; ++kb, ++it) {
                 const int s = it % STAGES;
                 if (!mbar_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1)) {
-                    *abort_flag = 1;
+                    give_up();
                     break;
                 }
                 const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
@@ -576,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // phases complete, every load of the pair has landed
         if (leader)
             for (int k = it > STAGES ? it - STAGES : 0; k < it; ++k)
-                mbar_wait(full0 + 8 * (k % STAGES), (k / STAGES) & 1);
+                if (!mbar_wait(full0 + 8 * (k % STAGES), (k / STAGES) & 1)) give_up();
     } else if (warp == 1 && leader && elect_one()) {
         // ---- MMA issuer (leader only)
         int it = 0, lt = 0;
@@ -622,10 +650,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 mma_commit_both(acc_full0 + 8 * acc);
                 ++lt;
             } while (kb < kblocks);
-            if (!ok) *abort_flag = 1;
+            if (!ok) give_up();
         }
         mma_commit_local_pair(mma_done);
-        mbar_wait(mma_done, 0);
+        if (!mbar_wait(mma_done, 0)) give_up();
     } else if (warp >= 2 && warp < 2 + kEpi) {
         // ---- epilogue (both CTAs): this CTA's 128 lanes of the accumulator,
         // a quarter per warp
@@ -848,6 +876,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // neither CTA leaves while the other may still signal it
+    if (threadIdx.x == 0 && *abort_flag) settle();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
