@@ -50,6 +50,12 @@ extern "C" {
 /* Largest number of groups of one call. */
 #define SWIGLU_MAX_GROUPS 1024
 
+/* Limits of the products' sizes (below; far beyond any memory but for the rows of
+ * an fp32 weight gradient, which must be summed within the 2 s of an internal wait). */
+#define SWIGLU_GROUPED_MAX_ROWS 2147483391
+#define SWIGLU_GROUPED_MAX_ROWS_F32 268435456
+#define SWIGLU_GROUPED_MAX_FEATURES 1073741823
+
 /*
  * Forward with an 8-bit checkpoint:
  *   y[r, j] = w[r] * silu(x[r, j]) * x[r, n + j]   (w NULL: no weights)
@@ -107,9 +113,11 @@ swiglu_status_t swiglu_ckpt8_bwd(const void *dy, const void *q, const void *scal
  *       q [rows, 2n] and scales [rows, 2 nb], the checkpoint of the unrounded
  *       g and u (both given or both NULL).
  *
- * Requirements: N (n) and K multiples of 8 and at least 8, rows below 2^31,
- * 1 <= groups <= SWIGLU_MAX_GROUPS, groups * N below 2^31 (else
- * SWIGLU_ERR_SHAPE); pointers 16-byte aligned, ends and probs 4-byte aligned
+ * Requirements: N (n) and K multiples of 8 and at least 8, rows at most
+ * SWIGLU_GROUPED_MAX_ROWS (an fp32 dW: SWIGLU_GROUPED_MAX_ROWS_F32), K and
+ * groups * N at most SWIGLU_GROUPED_MAX_FEATURES, groups * 2n as well,
+ * 1 <= groups <= SWIGLU_MAX_GROUPS, fewer than 2^29 tiles of 256 x 256 in a
+ * result (else SWIGLU_ERR_SHAPE); pointers 16-byte aligned, ends and probs 4-byte aligned
  * (else SWIGLU_ERR_STRIDE); outputs overlap nothing (SWIGLU_ERR_ALIAS).  No row
  * reads another group's rows, so a NaN in one row reaches no other row's
  * outputs and no other group's dW.  rows == 0 is an empty call (wgrad: every

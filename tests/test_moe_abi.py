@@ -132,3 +132,31 @@ def test_python_layer_refuses_cpu_tensors_and_wrong_shapes(sw):
         sw.swiglu_grouped_fc1_fwd(x, w, ends, save="fp4")
     with pytest.raises(ValueError, match="needs w"):
         sw.swiglu_ckpt8_bwd(torch.zeros(4, 8), torch.zeros(4, 16), torch.zeros(4, 2), dw=torch.zeros(4))
+
+
+def limit(name):
+    return int(re.search(rf"#define SWIGLU_GROUPED_{name} (\d+)\n", open(HEADER).read()).group(1))
+
+
+@pytest.mark.parametrize("product", ["fc1", "fwd", "dgrad", "wgrad"])
+def test_stated_limits_are_the_enforced_ones(sw, product):
+    """The largest sizes that the header allows get as far as the check of pointers, the
+    next ones do not."""
+    def call(rows=16, groups=3, N=32, K=32, **kw):
+        if product == "fc1":  # N counts gate and up rows
+            return fc1(sw, x=0, rows=rows, groups=groups, n=N // 2, K=K)
+        if product == "wgrad":
+            return wgrad(sw, dy=0, rows=rows, groups=groups, N=N, K=K, **kw)
+        return mm(sw, product, x=0, rows=rows, groups=groups, N=N, K=K)
+
+    rows, features = limit("MAX_ROWS"), limit("MAX_FEATURES")
+    assert call(rows=rows) == NULL and call(rows=rows + 1) == SHAPE
+    assert call(K=features // 8 * 8) == NULL and call(K=features // 8 * 8 + 8) == SHAPE
+    step = 16 if product == "fc1" else 8
+    for groups in (1, 3, 8, 1024):
+        N = features // groups // step * step
+        assert call(groups=groups, N=N) == NULL and call(groups=groups, N=N + step) == SHAPE
+    if product == "wgrad":
+        rows = limit("MAX_ROWS_F32")
+        for acc in (0, 1):
+            assert call(rows=rows, dwt=F32, acc=acc) == NULL and call(rows=rows + 1, dwt=F32, acc=acc) == SHAPE
