@@ -27,8 +27,9 @@ from . import (_DTYPE, SWIGLU_BF16, SwigluError, _on_device, _raw_stream, _rows_
 
 CKPT8_BLOCK = 32
 MAX_GROUPS = 1024
-Q_DTYPE = torch.float8_e4m3fn
-SCALE_DTYPE = torch.float8_e8m0fnu
+# None where torch has no such type: the other operators work all the same
+Q_DTYPE = getattr(torch, "float8_e4m3fn", None)
+SCALE_DTYPE = getattr(torch, "float8_e8m0fnu", None)
 
 # every symbol include/swiglu_moe.h declares
 MOE_EXPORTS = ("swiglu_ckpt8_fwd", "swiglu_ckpt8_bwd", "swiglu_grouped_fc1_fwd", "swiglu_grouped_mm_fwd",
@@ -111,11 +112,17 @@ def _float_type(t: torch.Tensor) -> int:
     return code
 
 
+def _need_checkpoint_types() -> None:
+    if Q_DTYPE is None or SCALE_DTYPE is None:
+        raise NotImplementedError("the 8-bit checkpoint needs a torch with float8_e4m3fn and float8_e8m0fnu")
+
+
 def swiglu_ckpt8_fwd(x: torch.Tensor, w: torch.Tensor = None, y: torch.Tensor = None, q: torch.Tensor = None,
                      scales: torch.Tensor = None, stream=None):
     """(y, q, scales): y = w[row] * silu(gate) * up and the 8-bit checkpoint of x.
 
     ``w`` (fp32, one weight per row of x) is optional."""
+    _need_checkpoint_types()
     shape, dtype, device = x.shape, x.dtype, x.device
     two_n = shape[-1]
     if two_n % 2:
@@ -150,6 +157,7 @@ def swiglu_ckpt8_bwd(dy: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, w:
     fp32 gradient of the row weights (None without ``w``) and, with ``return_y``
     (or a ``y`` given), the forward's output made again from the checkpoint
     (else None)."""
+    _need_checkpoint_types()
     if w is None and dw is not None:
         raise ValueError("dw is the gradient of w: it needs w")
     shape, dtype, device = dy.shape, dy.dtype, dy.device
@@ -234,6 +242,8 @@ def swiglu_grouped_fc1_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
     8-bit checkpoint."""
     if save not in (None, "bf16", "fp8"):
         raise ValueError('save must be None, "bf16" or "fp8"')
+    if save == "fp8":
+        _need_checkpoint_types()
     (rows, K), (E, two_n, wk) = _rows_and_experts(x, w, ends, "x")
     if wk != K or two_n % 2:
         raise ValueError("w must be [experts, 2n, K] with x's K")

@@ -160,3 +160,34 @@ def test_stated_limits_are_the_enforced_ones(sw, product):
         rows = limit("MAX_ROWS_F32")
         for acc in (0, 1):
             assert call(rows=rows, dwt=F32, acc=acc) == NULL and call(rows=rows + 1, dwt=F32, acc=acc) == SHAPE
+
+
+@pytest.mark.parametrize("missing", ["float8_e4m3fn", "float8_e8m0fnu"])
+def test_a_torch_without_the_checkpoint_types_keeps_the_rest(sw, missing):
+    """Such a torch imports the package; only the checkpoint's operators refuse."""
+    import subprocess
+    import sys
+
+    code = f"""
+import torch
+del torch.{missing}
+import gate_up_swiglu_gb300 as sw
+import gate_up_swiglu_gb300.experts
+x, w, ends = torch.zeros(4, 16).bfloat16(), torch.zeros(2, 32, 16).bfloat16(), torch.zeros(2, dtype=torch.int32)
+for fn in (lambda: sw.swiglu_gateup_fwd(x), lambda: sw.swiglu_grouped_fc1_fwd(x, w, ends, save="bf16"),
+           lambda: sw.swiglu_grouped_mm_fwd(x, w, ends)):
+    try:
+        fn()
+        assert False
+    except ValueError as e:
+        assert "CUDA" in str(e)
+for fn in (lambda: sw.swiglu_ckpt8_fwd(x), lambda: sw.swiglu_ckpt8_bwd(x, x, x),
+           lambda: sw.swiglu_grouped_fc1_fwd(x, w, ends, save="fp8")):
+    try:
+        fn()
+        assert False
+    except NotImplementedError as e:
+        assert "float8" in str(e)
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr[-2000:]
