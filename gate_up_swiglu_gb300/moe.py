@@ -242,6 +242,8 @@ def swiglu_grouped_fc1_fwd(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
     8-bit checkpoint."""
     if save not in (None, "bf16", "fp8"):
         raise ValueError('save must be None, "bf16" or "fp8"')
+    if (fc1 is not None and save != "bf16") or ((q is not None or scales is not None) and save != "fp8"):
+        raise ValueError('fc1 is written with save="bf16", q and scales with save="fp8"')
     if save == "fp8":
         _need_checkpoint_types()
     (rows, K), (E, two_n, wk) = _rows_and_experts(x, w, ends, "x")

@@ -191,3 +191,12 @@ for fn in (lambda: sw.swiglu_ckpt8_fwd(x), lambda: sw.swiglu_ckpt8_bwd(x, x, x),
 """
     run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_fc1_refuses_buffers_that_it_would_not_fill(sw):
+    x, w, ends = torch.zeros(4, 16).bfloat16(), torch.zeros(2, 32, 16).bfloat16(), torch.zeros(2, dtype=torch.int32)
+    buf = torch.zeros(4, 32)
+    for save, kw in ((None, dict(fc1=buf)), ("fp8", dict(fc1=buf)), (None, dict(q=buf)), (None, dict(scales=buf)),
+                     ("bf16", dict(q=buf, scales=buf)), ("bf16", dict(scales=buf))):
+        with pytest.raises(ValueError, match="is written with"):
+            sw.swiglu_grouped_fc1_fwd(x, w, ends, save=save, **kw)
