@@ -1411,18 +1411,42 @@ Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int spli
     return best;
 }
 
+// Rows of a tile of the split kernel, and its tiles at most, for a product over rows.
+int split_rows(int64_t rows) { return rows <= 32 ? 32 : 128; }
+
+template <int MODE>
+int64_t split_tiles(int64_t rows, int64_t groups, int64_t features) {
+    return most_tiles(rows, groups, features, kSplitF<MODE>, split_rows(rows));
+}
+
+template <int MODE>
+Plan plan_rows(int64_t rows, int64_t groups, int64_t features, int64_t depth) {
+    const int64_t same = rows < groups ? rows : groups, tiles = split_tiles<MODE>(rows, groups, features);
+    if (tiles > INT32_MAX / 16) return {0};
+    return plan(same, ceil_div(rows, same), features, kTileF<MODE>, kSplitF<MODE>, split_rows(rows), tiles,
+                ceil_div(depth, BK));
+}
+
+int64_t wgrad_split_tiles(int64_t groups, int64_t N, int64_t K) {
+    return groups * ceil_div(N, 128) * ceil_div(K, kSplitF<kWgrad>);
+}
+
+// An fp32 sum's slices stay within a segment.
+Plan plan_wgrad(int64_t rows, int64_t groups, int64_t N, int64_t K, bool f32) {
+    return plan(groups, N, K, 256, kSplitF<kWgrad>, 128, wgrad_split_tiles(groups, N, K),
+                ceil_div(ceil_div(rows, groups), BK), f32 ? ceil_div(rows, kSegmentRows) : 1);
+}
+
 // Launch a product over rows.
 template <int MODE>
 swiglu_status_t launch_rows(const Params &p, swiglu_stream_t stream) {
     const int64_t pairs = most_tiles(p.rows, p.groups, p.features, kTileF<MODE>, TILE_N);
     if (pairs > INT32_MAX / 4) return SWIGLU_ERR_SHAPE;
-    const bool few = p.rows <= 32;
-    const int64_t same = p.rows < p.groups ? p.rows : p.groups;
-    const int64_t tiles = most_tiles(p.rows, p.groups, p.features, kSplitF<MODE>, few ? 32 : 128);
-    const Plan pl = plan(same, ceil_div(p.rows, same), p.features, kTileF<MODE>, kSplitF<MODE>, few ? 32 : 128, tiles,
-                         ceil_div(p.depth, BK));
-    if (pl.size == 0 || tiles > INT32_MAX / 16) return launch_pairs<MODE>(p, pairs, stream);
-    return few ? launch_split<MODE, 32>(p, tiles, pl.size, stream) : launch_split<MODE, 128>(p, tiles, pl.size, stream);
+    const int size = plan_rows<MODE>(p.rows, p.groups, p.features, p.depth).size;
+    if (size == 0) return launch_pairs<MODE>(p, pairs, stream);
+    const int64_t tiles = split_tiles<MODE>(p.rows, p.groups, p.features);
+    return split_rows(p.rows) == 32 ? launch_split<MODE, 32>(p, tiles, size, stream)
+                                    : launch_split<MODE, 128>(p, tiles, size, stream);
 }
 
 // The checks that the products share.  A pair works off 64 rows of an fp32 weight
@@ -1595,16 +1619,14 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     p.f32_out = dw_dtype == SWIGLU_F32;
     p.accumulate = accumulate != 0;
     // Pairs: M is dW's rows, N its columns.  Split: the other way round, so that the
-    // lanes run along dW's rows; an fp32 sum's slices stay within a segment.
-    const int64_t split_tiles = groups * ceil_div(N, 128) * ceil_div(K, kSplitF<kWgrad>);
-    const Plan pl = plan(groups, N, K, 256, kSplitF<kWgrad>, 128, split_tiles, ceil_div(ceil_div(rows, groups), BK),
-                         p.f32_out ? ceil_div(rows, kSegmentRows) : 1);
-    if (pl.size > 0) {
+    // lanes run along dW's rows.
+    const int size = plan_wgrad(rows, groups, N, K, p.f32_out).size;
+    if (size > 0) {
         if (!map2(enc, &p.a, x, K, rows, BK) || !map2(enc, &p.b[0], dy, N, rows, BK))
             return moe::cuda_fail(cudaErrorInvalidValue);
         p.features = (int)K;
         p.cols = (int)N;
-        return launch_split<kWgrad, 128>(p, split_tiles, pl.size, stream);
+        return launch_split<kWgrad, 128>(p, wgrad_split_tiles(groups, N, K), size, stream);
     }
     if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK) ||
         !out_map(enc, &p.c, dw, eb, K, N, groups))
@@ -1615,6 +1637,29 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     p.features = (int)N;
     p.cols = (int)K;
     return launch_pairs<kWgrad>(p, pairs, stream);
+}
+
+swiglu_status_t swiglu_grouped_slices(swiglu_grouped_product_t product, int64_t rows, int64_t groups, int64_t N,
+                                      int64_t K, swiglu_dtype_t dw_dtype, int *slices) {
+    using namespace gmm;
+    if (slices == nullptr) return SWIGLU_ERR_NULL;
+    const swiglu_status_t st = check(rows, groups, N, K, SWIGLU_BF16);
+    if (st != SWIGLU_OK) return st;
+    if (product == SWIGLU_GROUPED_FC1 && 2 * N > SWIGLU_GROUPED_MAX_FEATURES / groups) return SWIGLU_ERR_SHAPE;
+    if (rows == 0) {
+        *slices = 0;
+        return SWIGLU_OK;
+    }
+    switch (product) {
+        case SWIGLU_GROUPED_FC1: *slices = plan_rows<kFc1>(rows, groups, N, K).size; return SWIGLU_OK;
+        case SWIGLU_GROUPED_MM: *slices = plan_rows<kMm>(rows, groups, N, K).size; return SWIGLU_OK;
+        case SWIGLU_GROUPED_DGRAD: *slices = plan_rows<kDgrad>(rows, groups, K, N).size; return SWIGLU_OK;
+        case SWIGLU_GROUPED_WGRAD:
+            if (dw_dtype != SWIGLU_BF16 && dw_dtype != SWIGLU_F32) return SWIGLU_ERR_DTYPE;
+            *slices = plan_wgrad(rows, groups, N, K, dw_dtype == SWIGLU_F32).size;
+            return SWIGLU_OK;
+    }
+    return SWIGLU_ERR_SHAPE;
 }
 
 swiglu_status_t swiglu_grouped_timeout_flag(int *flag) {

@@ -33,7 +33,8 @@ SCALE_DTYPE = getattr(torch, "float8_e8m0fnu", None)
 
 # every symbol include/swiglu_moe.h declares
 MOE_EXPORTS = ("swiglu_ckpt8_fwd", "swiglu_ckpt8_bwd", "swiglu_grouped_fc1_fwd", "swiglu_grouped_mm_fwd",
-               "swiglu_grouped_mm_dgrad", "swiglu_grouped_mm_wgrad", "swiglu_grouped_timeout_flag")
+               "swiglu_grouped_mm_dgrad", "swiglu_grouped_mm_wgrad", "swiglu_grouped_slices",
+               "swiglu_grouped_timeout_flag")
 
 
 def _declare() -> None:
@@ -45,6 +46,7 @@ def _declare() -> None:
             ("swiglu_grouped_mm_fwd", [vp] * 4 + [i64] * 4 + [i32, vp]),
             ("swiglu_grouped_mm_dgrad", [vp] * 4 + [i64] * 4 + [i32, vp]),
             ("swiglu_grouped_mm_wgrad", [vp] * 4 + [i64] * 4 + [i32, i32, i32, vp]),
+            ("swiglu_grouped_slices", [i32] + [i64] * 4 + [i32, ctypes.POINTER(ctypes.c_int)]),
             ("swiglu_grouped_timeout_flag", [ctypes.POINTER(ctypes.c_int)])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i32
@@ -307,6 +309,24 @@ def swiglu_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, ends: torch.Tenso
     return dw
 
 
+_PRODUCTS = ("fc1", "mm", "dgrad", "wgrad")
+
+
+def grouped_slices(product: str, rows: int, groups: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    """How a product ("fc1", with n as N, "mm", "dgrad" or "wgrad") of these sizes is
+    computed: 0, pairs of CTAs; else the CTAs that share a tile's contraction.
+    ``dtype`` is that of a weight gradient."""
+    if product not in _PRODUCTS:
+        raise ValueError(f"product must be one of {_PRODUCTS}")
+    if dtype not in _DTYPE:
+        raise ValueError("dtype must be float32 or bfloat16")
+    out = ctypes.c_int(0)
+    st = lib.swiglu_grouped_slices(_PRODUCTS.index(product), rows, groups, N, K, _DTYPE[dtype], ctypes.byref(out))
+    if st != 0:
+        raise SwigluError(st, "swiglu_grouped_slices")
+    return int(out.value)
+
+
 def grouped_timeout_flag() -> int:
     """1 if any grouped product so far gave up on an internal wait, else 0
     (synchronises with the current device)."""
@@ -318,5 +338,5 @@ def grouped_timeout_flag() -> int:
 
 
 __all__ = ["swiglu_ckpt8_fwd", "swiglu_ckpt8_bwd", "swiglu_grouped_fc1_fwd", "swiglu_grouped_mm_fwd",
-           "swiglu_grouped_mm_dgrad", "swiglu_grouped_mm_wgrad", "grouped_timeout_flag", "CKPT8_BLOCK", "MAX_GROUPS",
-           "MOE_EXPORTS"]
+           "swiglu_grouped_mm_dgrad", "swiglu_grouped_mm_wgrad", "grouped_slices", "grouped_timeout_flag", "CKPT8_BLOCK",
+           "MAX_GROUPS", "MOE_EXPORTS"]

@@ -142,6 +142,22 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
                                         int64_t K, swiglu_dtype_t dtype, swiglu_dtype_t dw_dtype,
                                         int accumulate, swiglu_stream_t stream);
 
+/* How a product of these sizes is computed (host only): *slices = 0, a pair of CTAs per
+ * tile of 256 x 256; 1, 2, 4 or 8, that many CTAs, each a slice of the contraction, per
+ * tile of 128 by at most 128.  N, K (fc1: n, K) and dw_dtype (read for the weight
+ * gradient) as in the call itself; the choice follows from the sizes alone, and sums are
+ * added in another order with another number of slices.  rows == 0: 0. */
+typedef enum {
+    SWIGLU_GROUPED_FC1 = 0,
+    SWIGLU_GROUPED_MM = 1,
+    SWIGLU_GROUPED_DGRAD = 2,
+    SWIGLU_GROUPED_WGRAD = 3
+} swiglu_grouped_product_t;
+
+swiglu_status_t swiglu_grouped_slices(swiglu_grouped_product_t product, int64_t rows,
+                                      int64_t groups, int64_t N, int64_t K,
+                                      swiglu_dtype_t dw_dtype, int *slices);
+
 /* *flag = 1 if any launch of the products above gave up on an internal wait so
  * far (its results are then undefined), else 0.  Synchronises with the current
  * device. */
