@@ -64,11 +64,14 @@ constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int TMEM_COLS = 2 * TILE_N;            // two accumulators
 constexpr int kMaxGroups = SWIGLU_MAX_GROUPS;
 constexpr int kGroupN = 16;          // N tiles per block of the tile order
-// fp32 weight gradients are summed in segments of this many rows: the tensor
-// cores' fp32 accumulation drops low bits at every step (a relative error of
-// about 1.1e-9 per row summed was measured: 4.4e-6 over 4096), and the segments
-// are added with rounded fp32 additions
+// Weight gradients are summed in segments of this many rows.  The tensor cores truncate
+// the running fp32 sum at every step of 16 rows, by less than 2^-23 of it: over rows of
+// one sign 1.4e-5 of the sum was measured for 4096, 3.9e-4 for 65,536 and 6.8e-3 for
+// 1,048,576 (of random signs 4.4e-6, 7.6e-5 and 1.2e-3).  The segments' sums are added
+// with rounded fp32 additions: fp32 results in dW itself, bf16 ones in tensor memory
+// (LONG below), whose drift then stays below a quarter of a rounding to bf16.
 constexpr int kSegmentRows = 4096;
+constexpr int kLongRows = 131072;
 
 constexpr int kTileSlots = 2;
 // byte offsets in the region after the ring
@@ -369,7 +372,33 @@ constexpr int kScheduler = 2 + kEpi;
 constexpr int kPairThreads = 32 * (3 + kEpi);
 static_assert(kEpi * STG_WARP_BYTES <= STG_BYTES && kEpi / 2 * STG_PAIR_FC1 <= STG_BYTES, "the epilogue's staging");
 
-template <int MODE>
+// The accumulator of the next accumulation and the parity of its barriers' phase; the
+// MMA thread and the epilogue's warps count alike.  The two take turns, but with LONG a
+// tile of more than one segment (`many`) sums each of them in the same accumulator and
+// holds the total of those before in the other.  The next tile takes the first one
+// again: when that is handed back, the total has been read too.
+template <bool LONG>
+struct Accumulators {
+    int n = 0;  // accumulations so far
+    int at = 0, used[2] = {0, 0};
+
+    __device__ __forceinline__ int index() const { return LONG ? at : n & 1; }
+    __device__ __forceinline__ int parity() const { return LONG ? (at == 0 ? used[0] : used[1]) & 1 : (n >> 1) & 1; }
+    __device__ __forceinline__ void next(bool many) {
+        if (LONG) {
+            if (at == 0)
+                ++used[0];
+            else
+                ++used[1];
+            if (!many) at ^= 1;
+        } else {
+            ++n;
+        }
+    }
+};
+
+// LONG (kWgrad with a bf16 result of more than kLongRows rows): see Accumulators.
+template <int MODE, bool LONG = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     grouped_mm_kernel(const __grid_constant__ Params p) {
     extern __shared__ unsigned char smem_raw[];
@@ -455,8 +484,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     };
     // columns of the instruction
     const auto width_of = [&](const Tile &t) { return MODE == kWgrad ? TILE_N : (t.cnt + 31) / 32 * 32; };
-    // contraction blocks per accumulation (kWgrad with fp32 results: a segment)
-    const int seg_blocks = MODE == kWgrad && p.f32_out ? kSegmentRows / BK : INT_MAX;
+    // contraction blocks per accumulation (kWgrad: a segment, where the sum has several)
+    const int seg_blocks = LONG ? kLongRows / BK : MODE == kWgrad && p.f32_out ? kSegmentRows / BK : INT_MAX;
 
     // tile k of this pair, for a single thread; group -1 when none is left
     const auto next_tile = [&](int k) {
@@ -607,7 +636,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (!mbar_wait(full0 + 8 * (k % STAGES), (k / STAGES) & 1)) give_up();
     } else if (warp == 1 && leader && elect_one()) {
         // ---- MMA issuer (leader only)
-        int it = 0, lt = 0;
+        int it = 0;
+        Accumulators<LONG> accs;
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const Tile t = next_tile(k);
@@ -617,8 +647,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int deep = MODE == kWgrad ? t.rows : p.depth;
             int kb = 0;
             do {  // one accumulation
-                const int acc = lt & 1;
-                if (!mbar_wait(acc_empty0 + 8 * acc, ((lt >> 1) & 1) ^ 1)) {
+                const int acc = accs.index();
+                if (!mbar_wait(acc_empty0 + 8 * acc, accs.parity() ^ 1)) {
                     ok = false;
                     break;
                 }
@@ -648,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
                 if (!ok) break;
                 mma_commit_both(acc_full0 + 8 * acc);
-                ++lt;
+                accs.next(kblocks > seg_blocks);
             } while (kb < kblocks);
             if (!ok) give_up();
         }
@@ -669,7 +699,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             __syncwarp();
         };
         const int bar_id = 1 + 2 * set + (quarter >> 1);
-        int lt = 0;
+        Accumulators<LONG> accs;
         bool ok = true;
         // the warp leaves the loop as one: the tile id, the abort flag and the
         // waits' outcome are warp-uniform
@@ -686,14 +716,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 kb = kblocks - kb > seg_blocks ? kb + seg_blocks : kblocks;
                 // a later segment adds to what the one before it has written
                 if (MODE == kWgrad && !first && elect_one()) bulk_wait<0>();
-                const int acc = lt & 1;
+                const int acc = accs.index();
                 // after a wait that ran out the values are undefined, but the warps
                 // stay in step and the accumulator is handed back
-                if (!__all_sync(0xffffffffu, mbar_wait(acc_full0 + 8 * acc, (lt >> 1) & 1))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(acc_full0 + 8 * acc, accs.parity()))) {
                     if (lane == 0) *abort_flag = 1;
                     ok = MODE == kFc1;  // (a pair leaves at the next tile id)
                 }
-                ++lt;
+                accs.next(kblocks > seg_blocks);
                 tc_fence_after();
                 const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
                 if (kChunk * set >= width) {  // no columns for this warp
@@ -712,11 +742,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         tmem_load32(tbase + c, v);
                     }
                     tmem_wait_ld();
+                    if constexpr (LONG) {
+                        const uint32_t total = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)((acc ^ 1) * TILE_N);
+                        if (!first) {
+                            uint32_t before[kChunk];
+                            tmem_load32(total + c, before);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < kChunk; ++i)
+                                v[i] = __float_as_uint(__fadd_rn(__uint_as_float(before[i]), __uint_as_float(v[i])));
+                        }
+                        if (kb < kblocks) {
+                            tmem_store32(total + c, v);
+                            tmem_wait_st();
+                        }
+                    }
                     if (c + kStep >= width) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
                     }
+                    if (LONG && kb < kblocks) continue;
                     if (kblocks == 0) {  // nothing was accumulated
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i) v[i] = 0u;
@@ -1327,7 +1373,7 @@ constexpr int kSms = 152;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // One cluster per tile, of which there are `clusters` at most.
-template <int MODE>
+template <int MODE, bool LONG = false>
 swiglu_status_t launch_pairs(const Params &p, int64_t clusters, swiglu_stream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1336,11 +1382,11 @@ swiglu_status_t launch_pairs(const Params &p, int64_t clusters, swiglu_stream_t 
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (!(dev >= 0 && dev < kMaxDevices && attr_set[dev].load())) {
-        e = cudaFuncSetAttribute(grouped_mm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        e = cudaFuncSetAttribute(grouped_mm_kernel<MODE, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
         if (e != cudaSuccess) return moe::cuda_fail(e);
         if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true);
     }
-    e = moe::launch(grouped_mm_kernel<MODE>, dim3((unsigned)(2 * clusters)), kPairThreads, SMEM_BYTES,
+    e = moe::launch(grouped_mm_kernel<MODE, LONG>, dim3((unsigned)(2 * clusters)), kPairThreads, SMEM_BYTES,
                     stream, 0, p);
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
@@ -1431,10 +1477,10 @@ int64_t wgrad_split_tiles(int64_t groups, int64_t N, int64_t K) {
     return groups * ceil_div(N, 128) * ceil_div(K, kSplitF<kWgrad>);
 }
 
-// An fp32 sum's slices stay within a segment.
+// A sum's slices stay within a segment.
 Plan plan_wgrad(int64_t rows, int64_t groups, int64_t N, int64_t K, bool f32) {
     return plan(groups, N, K, 256, kSplitF<kWgrad>, 128, wgrad_split_tiles(groups, N, K),
-                ceil_div(ceil_div(rows, groups), BK), f32 ? ceil_div(rows, kSegmentRows) : 1);
+                ceil_div(ceil_div(rows, groups), BK), ceil_div(rows, f32 ? kSegmentRows : kLongRows));
 }
 
 // Launch a product over rows.
@@ -1449,10 +1495,9 @@ swiglu_status_t launch_rows(const Params &p, swiglu_stream_t stream) {
                                     : launch_split<MODE, 128>(p, tiles, size, stream);
 }
 
-// The checks that the products share.  A pair works off 64 rows of an fp32 weight
-// gradient in 0.27 us, one segment after the other, while its tile's readers wait for
-// the next tile: 1.1 s for SWIGLU_GROUPED_MAX_ROWS_F32 rows of one group.  (A sum in
-// bf16 of as many rows, whose tiles must be few to fit the memory, is cut into slices.)
+// The checks that the products share.  A pair works off 64 rows of a weight gradient in
+// 0.27 us, one segment after the other, while its tile's readers wait for the next tile:
+// 1.1 s for SWIGLU_GROUPED_MAX_ROWS_WGRAD rows of one group.
 static_assert(SWIGLU_GROUPED_MAX_ROWS == INT32_MAX - TILE_N && SWIGLU_GROUPED_MAX_FEATURES == INT32_MAX / 2,
               "rows rounded up to a tile, and twice the features, fit an int");
 swiglu_status_t check(int64_t rows, int64_t groups, int64_t features, int64_t K, swiglu_dtype_t dtype) {
@@ -1588,7 +1633,7 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     if (st != SWIGLU_OK) return st;
     if (dw_dtype != SWIGLU_BF16 && dw_dtype != SWIGLU_F32) return SWIGLU_ERR_DTYPE;
     if (accumulate != 0 && dw_dtype != SWIGLU_F32) return SWIGLU_ERR_DTYPE;
-    if (dw_dtype == SWIGLU_F32 && rows > SWIGLU_GROUPED_MAX_ROWS_F32) return SWIGLU_ERR_SHAPE;
+    if (rows > SWIGLU_GROUPED_MAX_ROWS_WGRAD) return SWIGLU_ERR_SHAPE;
     const int eb = dw_dtype == SWIGLU_F32 ? 4 : 2;
     Span sdw;
     if (!span_of(dw, groups * N, K, K, eb, sdw)) return SWIGLU_ERR_SHAPE;
@@ -1636,6 +1681,7 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
             return moe::cuda_fail(cudaErrorInvalidValue);
     p.features = (int)N;
     p.cols = (int)K;
+    if (!p.f32_out && rows > kLongRows) return launch_pairs<kWgrad, true>(p, pairs, stream);
     return launch_pairs<kWgrad>(p, pairs, stream);
 }
 
@@ -1656,6 +1702,7 @@ swiglu_status_t swiglu_grouped_slices(swiglu_grouped_product_t product, int64_t 
         case SWIGLU_GROUPED_DGRAD: *slices = plan_rows<kDgrad>(rows, groups, K, N).size; return SWIGLU_OK;
         case SWIGLU_GROUPED_WGRAD:
             if (dw_dtype != SWIGLU_BF16 && dw_dtype != SWIGLU_F32) return SWIGLU_ERR_DTYPE;
+            if (rows > SWIGLU_GROUPED_MAX_ROWS_WGRAD) return SWIGLU_ERR_SHAPE;
             *slices = plan_wgrad(rows, groups, N, K, dw_dtype == SWIGLU_F32).size;
             return SWIGLU_OK;
     }

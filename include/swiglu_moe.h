@@ -51,9 +51,9 @@ extern "C" {
 #define SWIGLU_MAX_GROUPS 1024
 
 /* Limits of the products' sizes (below; far beyond any memory but for the rows of
- * an fp32 weight gradient, which must be summed within the 2 s of an internal wait). */
+ * a weight gradient, which must be summed within the 2 s of an internal wait). */
 #define SWIGLU_GROUPED_MAX_ROWS 2147483391
-#define SWIGLU_GROUPED_MAX_ROWS_F32 268435456
+#define SWIGLU_GROUPED_MAX_ROWS_WGRAD 268435456
 #define SWIGLU_GROUPED_MAX_FEATURES 1073741823
 
 /*
@@ -94,6 +94,10 @@ swiglu_status_t swiglu_ckpt8_bwd(const void *dy, const void *q, const void *scal
 /*
  * The experts' products (bf16 only, fp32 accumulation on the tensor cores,
  * every result rounded once; contiguous tensors, 16-byte aligned pointers).
+ * The tensor cores truncate the running sum every 16 terms: a sum of D terms is
+ * within D 2^-27 of the sum of their absolute values.  D is the depth of a
+ * product over rows; weight gradients add up sums of at most 4096 (fp32 dW) or
+ * 131,072 rows (bf16 dW) with rounded fp32 additions.
  * For each row t of group e:
  *
  *   swiglu_grouped_mm_fwd     y[t, :]  = W[e] x[t, :]
@@ -114,7 +118,7 @@ swiglu_status_t swiglu_ckpt8_bwd(const void *dy, const void *q, const void *scal
  *       g and u (both given or both NULL).
  *
  * Requirements: N (n) and K multiples of 8 and at least 8, rows at most
- * SWIGLU_GROUPED_MAX_ROWS (an fp32 dW: SWIGLU_GROUPED_MAX_ROWS_F32), K and
+ * SWIGLU_GROUPED_MAX_ROWS (dW: SWIGLU_GROUPED_MAX_ROWS_WGRAD), K and
  * groups * N at most SWIGLU_GROUPED_MAX_FEATURES, groups * 2n as well,
  * 1 <= groups <= SWIGLU_MAX_GROUPS, fewer than 2^29 tiles of 256 x 256 in a
  * result (else SWIGLU_ERR_SHAPE); pointers 16-byte aligned, ends and probs 4-byte aligned

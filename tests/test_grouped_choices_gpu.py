@@ -236,3 +236,42 @@ def test_module_by_pairs(sw, checkpoint):
                             ("dprobs", probs.grad, dp), ("dw1", m.w1.grad, R.wgrad(dfc1, xd, ends, E)[0]),
                             ("dw2", m.w2.grad, R.wgrad(dout, y2, ends, E)[0])):
         assert float((got.detach().double() - want).norm() / want.norm()) < 1e-2, name
+
+
+def test_bf16_weight_gradients_over_many_rows(sw):
+    """A bf16 dW over more rows than one running sum may have, by pairs: long and short
+    groups in turn, with NaN rows behind; integers, so that every sum is exact."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    counts, N, K = [300, 270_000, 0, 5, 131_072, 140_001, 700], 1032, 1288
+    rows, E, ends = sum(counts) + 100, len(counts), _ends(counts)
+    assert sw.grouped_slices("wgrad", rows, E, N, K) == 0
+    x, dy = _ints(g, rows, K, top=1), _ints(g, rows, N, top=2)
+    x[-100:], dy[-100:] = float("nan"), float("nan")
+    got = sw.swiglu_grouped_mm_wgrad(dy, x, ends)
+    at = 0
+    for e, c in enumerate(counts):
+        want = torch.zeros(N, K, dtype=torch.float64, device="cuda")
+        for r in range(at, at + c, 65536):
+            t = min(r + 65536, at + c)
+            want += dy[r:t].double().T @ x[r:t].double()
+        at += c
+        assert torch.equal(_bits(got[e]), _bits(want.bfloat16())), f"group of {c} rows"
+
+
+@pytest.mark.parametrize("N,K,slices", [(2056, 2048, 0), (128, 136, 8)])
+def test_bf16_weight_gradients_keep_their_precision(sw, N, K, slices):
+    """600,000 rows of one sign.  Each step of 16 rows truncates the running sum by less
+    than 2^-23 of it, so 131,072 rows lose at most 2^13 2^-23 = 2^-10; with the rounding
+    to bf16 (8 significant bits: 2^-8) and of the additions every value is within 2^-8 +
+    2^-10 + 2^-20.  One running sum would lose 3.8e-3 on average."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rows = 600_000
+    assert sw.grouped_slices("wgrad", rows, 1, N, K) == slices
+    x = torch.randn(rows, K, generator=g, device="cuda").bfloat16().abs()
+    dy = torch.randn(rows, N, generator=g, device="cuda").bfloat16().abs()
+    some = torch.arange(0, N, 37, device="cuda")  # rows of dW
+    got = sw.swiglu_grouped_mm_wgrad(dy, x, _ends([rows]))[0][some]
+    want = torch.zeros(len(some), K, dtype=torch.float64, device="cuda")
+    for r in range(0, rows, 65536):
+        want += dy[r:r + 65536, some].double().T @ x[r:r + 65536].double()
+    assert float(((got.double() - want).abs() / want).max()) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -20

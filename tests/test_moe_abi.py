@@ -149,7 +149,7 @@ def test_stated_limits_are_the_enforced_ones(sw, product):
             return wgrad(sw, dy=0, rows=rows, groups=groups, N=N, K=K, **kw)
         return mm(sw, product, x=0, rows=rows, groups=groups, N=N, K=K)
 
-    rows, features = limit("MAX_ROWS"), limit("MAX_FEATURES")
+    rows, features = limit("MAX_ROWS_WGRAD" if product == "wgrad" else "MAX_ROWS"), limit("MAX_FEATURES")
     assert call(rows=rows) == NULL and call(rows=rows + 1) == SHAPE
     assert call(K=features // 8 * 8) == NULL and call(K=features // 8 * 8 + 8) == SHAPE
     step = 16 if product == "fc1" else 8
@@ -157,7 +157,6 @@ def test_stated_limits_are_the_enforced_ones(sw, product):
         N = features // groups // step * step
         assert call(groups=groups, N=N) == NULL and call(groups=groups, N=N + step) == SHAPE
     if product == "wgrad":
-        rows = limit("MAX_ROWS_F32")
         for acc in (0, 1):
             assert call(rows=rows, dwt=F32, acc=acc) == NULL and call(rows=rows + 1, dwt=F32, acc=acc) == SHAPE
 
