@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(T) ckpt8_bwd_narrow_kernel(const BwdParams p) 
 //
 // Times (bf16, with y where it says so, of the 6680 GB/s copy): [8192, 2 x 4096]
 // 44.7 us 0.91, with y 52.5 us 0.96; [8192, 2 x 14336] 143 us 0.99.  Registers held
-// to 8 CTAs of 128 threads for 32-byte packs (45.9 us unbound, 62.9 us at 10).
+// to 8 CTAs of 128 threads for 32-byte packs (45.9 us unbound, 62.9 us at 10; measured
+// with a CTA per row, the warp per row takes the same bound).
 template <typename E, int VEC, int T, int ROWS>
 __global__ void __launch_bounds__(T, E::kBytes * VEC == 32 && T == 128 ? 8 : 0) ckpt8_bwd_weighted_kernel(const BwdParams p) {
     swiglu::await_previous_grid();

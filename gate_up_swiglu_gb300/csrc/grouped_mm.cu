@@ -17,8 +17,8 @@
 // The weight gradient has W's rows as M and its columns as N.  A block of 64 of the
 // contraction takes a pair 516 cycles at 256 rows, where the tensor cores need 512;
 // a tile of w rows fewer is bound by the SM's 64 bytes a cycle from L2, 256 + w
-// cycles.  16384 rows over 8 groups of [8192, 4096]: 1970 - 2040 TFLOP/s forward and
-// fc1, 1905 - 1970 and 1946 - 2010 the gradients, by the power that the GPU allows.
+// cycles.  16384 rows over 8 groups of [14336, 4096], at the GPU's power limit: 1735
+// TFLOP/s forward, 1672 fc1 with its checkpoint, 1655 and 1705 the gradients.
 //
 // Operand tiles are 64 elements of the contraction deep, 128-byte swizzle.
 // Where the contraction runs along memory rows the tile is K-major; the data
@@ -1422,14 +1422,16 @@ swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_st
 // rates the two kernels reach, times the rounds of the grid, plus what a launch,
 // a tile, the joining of the sums and the CTAs beyond the last tile take.  The
 // constants are a fit to the times of all five choices on 14,500 shapes (forward,
-// fc1 and both gradients; 1 to 32768 rows, 1 to 64 groups, widths 64 to 14336); with
-// them the choice is on average 2.4 % slower than the best one, where always pairs
-// are 22 % and always one CTA per tile 36 % slower.
+// fc1 and both gradients; 1 to 32768 rows, 1 to 64 equal groups, widths 64 to 14336);
+// with them the choice is on average 2.4 % slower than the best one, where always pairs
+// are 22 % and always one CTA per tile 36 % slower.  (A weight gradient's pairs multiply
+// 256 columns whatever N is; with that in place of N's own width the choice was no
+// better, 2.5 % off the best against 2.3 % on 384 shapes with N below 256.)
 struct Plan {
     int size;  // CTAs per tile of the split kernel; 0: pairs
 };
 
-// `same` groups of `rows_per` rows (kWgrad: of dW's columns) by `features`; pair_f
+// `same` groups of `rows_per` rows (kWgrad: dW's rows, N) by `features`; pair_f
 // and split_f: features of a tile, nt: rows of a tile of the split kernel, most: its
 // tiles at most; least_size: the fewest slices a sum may be cut into (pairs cut it
 // themselves).
