@@ -244,6 +244,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    // a wait of this thread ran out: both CTAs stop (see settle; the epilogue's warps set
+    // their own CTA's flag alone, and the MMA thread, left without operands, tells both)
+    const auto give_up = [&]() {
+        *abort_flag = 1;
+        store_cluster(map_to_rank(st0 + OFF_ABORT, rank ^ 1u), 1);
+    };
+
     if (warp == 0 && lane == 0) {
         // ---- producer (both CTAs): this CTA's X rows and its half of the W
         // slab for each tile.  The leader's producer also schedules: it
@@ -259,12 +266,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int slot = k % kTileSlots;
             if (leader) {
                 if (!mbar_wait<true>(tile_empty0 + 8 * slot, ((k / kTileSlots) & 1) ^ 1)) {
-                    *abort_flag = 1;
+                    give_up();
                     tile = -1;
                 }
                 publish_tile(tile_ids_addr, tile_full0, slot, tile);
             } else {
-                tile = mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1) ? tile_ids[slot] : -1;
+                tile = -1;
+                if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1))
+                    tile = tile_ids[slot];
+                else
+                    give_up();
                 mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
             }
             if (tile < 0) break;
@@ -281,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 const int s = it % STAGES2;
                 if (!mbar_wait(empty0 + 8 * s, ((it / STAGES2) & 1) ^ 1)) {
-                    *abort_flag = 1;
+                    give_up();
                     break;
                 }
                 const uint32_t full_leader = map_to_rank(full0 + 8 * s, 0);
@@ -293,12 +304,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // the answer is waited for even after an abort, so it never
                 // lands in shared memory the CTA has left
                 int next = -1;
-                if (asked && mbar_wait<true>(clc_bar, asks++ & 1)) {
+                if (asked && !mbar_wait<true>(clc_bar, asks++ & 1)) {
+                    give_up();
+                } else if (asked) {
                     const int x = clc_cancelled_cta(clc_resp);
                     if (x >= 0) {
                         next = x >> 1;
                         if ((x & 1) != 0 || next >= tiles) {  // not a cluster's first CTA of this grid
-                            *abort_flag = 1;
+                            give_up();
                             atomicExch(&g_fc1_timeout, 1);
                             next = -1;
                         }
@@ -311,18 +324,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // phases complete, every load of the pair has landed
         if (leader)
             for (int k = it > STAGES2 ? it - STAGES2 : 0; k < it; ++k)
-                mbar_wait(full0 + 8 * (k % STAGES2), (k / STAGES2) & 1);
+                if (!mbar_wait(full0 + 8 * (k % STAGES2), (k / STAGES2) & 1)) give_up();
     } else if (warp == 1 && lane == 0 && leader) {
         // ---- MMA issuer (leader only): drives the tensor cores of both SMs
         int it = 0, lt = 0;
         for (int k = 0;; ++k, ++lt) {
             const int slot = k % kTileSlots;
-            const int tile = mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1) ? tile_ids[slot] : -1;
+            int tile = -1;
+            if (mbar_wait<true>(tile_full0 + 8 * slot, (k / kTileSlots) & 1))
+                tile = tile_ids[slot];
+            else
+                give_up();
             mbar_arrive_cluster(tile_empty_leader0 + 8 * slot);
             if (tile < 0 || *abort_flag) break;
             const int acc = lt & 1;
             if (!mbar_wait(acc_empty0 + 8 * acc, ((lt >> 1) & 1) ^ 1)) {
-                *abort_flag = 1;
+                give_up();
                 break;
             }
             tc_fence_after();
@@ -344,13 +361,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mma_commit_both(empty0 + 8 * s);
             }
             if (!ok) {
-                *abort_flag = 1;
+                give_up();
                 break;
             }
             mma_commit_both(acc_full0 + 8 * acc);
         }
         mma_commit_local_pair(mma_done);
-        mbar_wait(mma_done, 0);
+        if (!mbar_wait(mma_done, 0)) give_up();
     } else if (warp >= 2) {
         // ---- epilogue (both CTAs): this CTA's 128 rows of the accumulator
         const int quarter = warp & 3;
@@ -423,6 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // neither CTA leaves while the other may still signal it
+    if (threadIdx.x == 0 && *abort_flag) settle();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),

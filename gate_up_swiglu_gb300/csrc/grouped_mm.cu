@@ -107,18 +107,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return mbar_wait_or_flag<kCluster>(bar, parity, &g_timeout);
 }
 
-// A pair of which a wait ran out may leave loads of either CTA in flight that nobody
-// waits for (each counts on a barrier of the leader, whose phase the other CTA's part
-// may never complete), or an answer of the launch control.  So whoever gives up tells
-// both CTAs, and after their last meeting, when nothing more is issued, both keep their
-// shared memory for 10 ms, thousands of times what a load takes.
-constexpr unsigned long long kSettleNs = 10000000ull;
-
-__device__ __noinline__ void settle() {
-    const uint64_t t0 = now_ns();
-    while (now_ns() - t0 < kSettleNs) __nanosleep(1000);
-}
-
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -473,8 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // that writes mostly zeros.)
     const auto give_up = [&]() {
         *abort_flag = 1;
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(st0 + OFF_ABORT, rank ^ 1u)), "r"(1)
-                     : "memory");
+        store_cluster(map_to_rank(st0 + OFF_ABORT, rank ^ 1u), 1);
     };
 
     // contraction blocks of a tile

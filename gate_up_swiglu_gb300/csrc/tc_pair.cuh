@@ -257,6 +257,22 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
     return out;
 }
 
+__device__ __forceinline__ void store_cluster(uint32_t addr_cluster, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr_cluster), "r"(v) : "memory");
+}
+
+// A pair of which a wait ran out may leave loads of either CTA in flight that nobody
+// waits for (each counts on a barrier of the leader, whose phase the other CTA's part
+// may never complete), or an answer of the launch control.  So whoever gives up tells
+// both CTAs, and after their last meeting, when nothing more is issued, both keep their
+// shared memory for 10 ms, thousands of times what a load takes.
+constexpr unsigned long long kSettleNs = 10000000ull;
+
+static __device__ __noinline__ void settle() {
+    const uint64_t t0 = now_ns();
+    while (now_ns() - t0 < kSettleNs) __nanosleep(1000);
+}
+
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");

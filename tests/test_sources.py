@@ -32,15 +32,18 @@ def test_shared_memory_loads_stay_behind_their_barriers(path):
             assert re.match(r"asm\s+volatile", s) and '"memory"' in s, f"{os.path.basename(path)}:{line}"
 
 
-def test_a_pair_that_gave_up_stays_until_its_loads_have_landed():
-    """grouped_mm_kernel: the threads that issue work tell both CTAs that a wait ran out,
-    and after their last meeting one thread of each waits for what is in flight."""
-    text = open(os.path.join(CSRC, "grouped_mm.cu")).read()
-    kernel = text[text.index("grouped_mm_kernel(const __grid_constant__"):]
+@pytest.mark.parametrize("name,kernel_name,roles,sites", [
+    # scheduler: slot, answer, bad answer; producer: tile, stage, landing; MMA: tile, its two, the last commit
+    ("grouped_mm.cu", "grouped_mm_kernel", ("if (warp == kScheduler)", "// ---- epilogue"), 7),
+    ("fc1_swiglu.cu", "fc1_swiglu_pair_kernel", ("// ---- producer", "// ---- epilogue"), 10)])
+def test_a_pair_that_gave_up_stays_until_its_loads_have_landed(name, kernel_name, roles, sites):
+    """The threads of a pair that issue work tell both CTAs that a wait ran out, and after
+    their last meeting one thread of each waits for what is in flight."""
+    text = open(os.path.join(CSRC, name)).read()
+    kernel = text[text.index(kernel_name + "(const __grid_constant__"):]
     kernel = kernel[:kernel.index("\n}\n")]
     last = kernel[kernel.rindex("cluster_sync();"):]
     assert "if (threadIdx.x == 0 && *abort_flag) settle();" in last
-    roles = kernel[kernel.index("if (warp == kScheduler)"):kernel.index("// ---- epilogue")]
-    # scheduler: slot, answer, bad answer; producer: stage, landing; MMA: any of its two, the last commit
-    assert roles.count("give_up();") == 7 and "*abort_flag = 1" not in roles
-    assert re.search(r"void settle\(\) \{[^}]*kSettleNs", text)
+    part = kernel[kernel.index(roles[0]):kernel.index(roles[1])]
+    assert part.count("give_up();") == sites and "*abort_flag = 1" not in part
+    assert re.search(r"void settle\(\) \{[^}]*kSettleNs", open(os.path.join(CSRC, "tc_pair.cuh")).read())
