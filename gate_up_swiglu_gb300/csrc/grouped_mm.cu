@@ -64,13 +64,17 @@ constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int TMEM_COLS = 2 * TILE_N;            // two accumulators
 constexpr int kMaxGroups = SWIGLU_MAX_GROUPS;
 constexpr int kGroupN = 16;          // N tiles per block of the tile order
-// Weight gradients are summed in segments of this many rows.  The tensor cores truncate
-// the running fp32 sum at every step of 16 rows, by less than 2^-23 of it: over rows of
-// one sign 1.4e-5 of the sum was measured for 4096, 3.9e-4 for 65,536 and 6.8e-3 for
-// 1,048,576 (of random signs 4.4e-6, 7.6e-5 and 1.2e-3).  The segments' sums are added
-// with rounded fp32 additions: fp32 results in dW itself, bf16 ones in tensor memory
-// (LONG below), whose drift then stays below a quarter of a rounding to bf16.
-constexpr int kSegmentRows = 4096;
+// The tensor cores truncate the running fp32 sum at every step of 16 terms, by less
+// than 2^-23 of it: for a weight gradient over rows of one sign 1.4e-5 of the sum was
+// measured for 4096 rows, 3.9e-4 for 65,536 and 6.8e-3 for 1,048,576 (of random signs
+// 4.4e-6, 7.6e-5 and 1.2e-3).  Where more than kSegmentRows (fp32 result) or kLongRows
+// (bf16: a quarter of its rounding) could meet in one sum, the kernels with SUMS add
+// up segments of kSegmentRows with rounded additions, in the epilogue's registers: the
+// two accumulators take turns, and while one is read the other is summed in.  What is
+// left in fp32: 9e-7 of one sign, 5e-7 of random signs, over any number of rows.  Eight
+// groups of 2048 rows, [4096, 7168]: 634 us, 618 in one sum each; 6932 rows, [5224, 10240],
+// 509 us, 548 with segments of 4096 rows that were added in dW.
+constexpr int kSegmentRows = 512;
 constexpr int kLongRows = 131072;
 
 constexpr int kTileSlots = 2;
@@ -360,33 +364,7 @@ constexpr int kScheduler = 2 + kEpi;
 constexpr int kPairThreads = 32 * (3 + kEpi);
 static_assert(kEpi * STG_WARP_BYTES <= STG_BYTES && kEpi / 2 * STG_PAIR_FC1 <= STG_BYTES, "the epilogue's staging");
 
-// The accumulator of the next accumulation and the parity of its barriers' phase; the
-// MMA thread and the epilogue's warps count alike.  The two take turns, but with LONG a
-// tile of more than one segment (`many`) sums each of them in the same accumulator and
-// holds the total of those before in the other.  The next tile takes the first one
-// again: when that is handed back, the total has been read too.
-template <bool LONG>
-struct Accumulators {
-    int n = 0;  // accumulations so far
-    int at = 0, used[2] = {0, 0};
-
-    __device__ __forceinline__ int index() const { return LONG ? at : n & 1; }
-    __device__ __forceinline__ int parity() const { return LONG ? (at == 0 ? used[0] : used[1]) & 1 : (n >> 1) & 1; }
-    __device__ __forceinline__ void next(bool many) {
-        if (LONG) {
-            if (at == 0)
-                ++used[0];
-            else
-                ++used[1];
-            if (!many) at ^= 1;
-        } else {
-            ++n;
-        }
-    }
-};
-
-// LONG (kWgrad with a bf16 result of more than kLongRows rows): see Accumulators.
-template <int MODE, bool LONG = false>
+template <int MODE, bool SUMS = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     grouped_mm_kernel(const __grid_constant__ Params p) {
     extern __shared__ unsigned char smem_raw[];
@@ -471,8 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     };
     // columns of the instruction
     const auto width_of = [&](const Tile &t) { return MODE == kWgrad ? TILE_N : (t.cnt + 31) / 32 * 32; };
-    // contraction blocks per accumulation (kWgrad: a segment, where the sum has several)
-    const int seg_blocks = LONG ? kLongRows / BK : MODE == kWgrad && p.f32_out ? kSegmentRows / BK : INT_MAX;
+    // contraction blocks per accumulation
+    constexpr int kSegBlocks = SUMS ? kSegmentRows / BK : INT_MAX;
 
     // tile k of this pair, for a single thread; group -1 when none is left
     const auto next_tile = [&](int k) {
@@ -623,8 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (!mbar_wait(full0 + 8 * (k % STAGES), (k / STAGES) & 1)) give_up();
     } else if (warp == 1 && leader && elect_one()) {
         // ---- MMA issuer (leader only)
-        int it = 0;
-        Accumulators<LONG> accs;
+        int it = 0, lt = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const Tile t = next_tile(k);
@@ -634,14 +611,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int deep = MODE == kWgrad ? t.rows : p.depth;
             int kb = 0;
             do {  // one accumulation
-                const int acc = accs.index();
-                if (!mbar_wait(acc_empty0 + 8 * acc, accs.parity() ^ 1)) {
+                const int acc = lt & 1;
+                if (!mbar_wait(acc_empty0 + 8 * acc, ((lt >> 1) & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * TILE_N);
-                const int first = kb, last = kblocks - kb > seg_blocks ? kb + seg_blocks : kblocks;
+                const int first = kb, last = kblocks - kb > kSegBlocks ? kb + kSegBlocks : kblocks;
                 for (; kb < last; ++kb, ++it) {
                     const int s = it % STAGES;
                     if (!mbar_wait(full0 + 8 * s, (it / STAGES) & 1)) {
@@ -665,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
                 if (!ok) break;
                 mma_commit_both(acc_full0 + 8 * acc);
-                accs.next(kblocks > seg_blocks);
+                ++lt;
             } while (kb < kblocks);
             if (!ok) give_up();
         }
@@ -685,8 +662,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (elect_one()) bulk_wait_read<0>();
             __syncwarp();
         };
+        // kWgrad: 32 columns of a tile, from column c on.  A lane is a row of dW; stores
+        // beyond its rows and columns are cut off by the tensor map.
+        const auto put_weights = [&](const Tile &t, const uint32_t (&v)[kChunk], int c) {
+            if constexpr (MODE == kWgrad) {
+                const int row0 = t.m0 + 128 * (int)rank + 32 * quarter;
+                const int swz = (lane >> 1) & 3;
+                if (p.f32_out) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        free_buffer();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4 *>(to + lane * 64 + ((i ^ swz) << 4)) =
+                                make_uint4(v[16 * h + 4 * i], v[16 * h + 4 * i + 1], v[16 * h + 4 * i + 2],
+                                           v[16 * h + 4 * i + 3]);
+                        fence_async_shared();
+                        __syncwarp();
+                        const bool in = row0 < p.features && t.n0 + c + 16 * h < p.cols;
+                        if (elect_one()) {
+                            if (in && p.accumulate)
+                                tma_add_3d(&p.c, smem_addr(to), t.n0 + c + 16 * h, row0, t.group);
+                            else if (in)
+                                tma_store_3d(&p.c, smem_addr(to), t.n0 + c + 16 * h, row0, t.group);
+                            bulk_commit();
+                        }
+                    }
+                } else {
+                    free_buffer();
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        swiglu::BF16::put2(w, i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(to + lane * 64 + ((i ^ swz) << 4)) =
+                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (elect_one()) {
+                        if (row0 < p.features && t.n0 + c < p.cols)
+                            tma_store_3d(&p.c, smem_addr(to), t.n0 + c, row0, t.group);
+                        bulk_commit();
+                    }
+                }
+            }
+        };
         const int bar_id = 1 + 2 * set + (quarter >> 1);
-        Accumulators<LONG> accs;
+        int lt = 0;
         bool ok = true;
         // the warp leaves the loop as one: the tile id, the abort flag and the
         // waits' outcome are warp-uniform
@@ -697,212 +720,189 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (MODE == kFc1 ? any_of_pair(bar_id, t.group < 0) : t.group < 0) break;
             const int kblocks = blocks_of(t);
             const int width = width_of(t);
-            int kb = 0;
-            do {
-                const bool first = kb == 0;
-                kb = kblocks - kb > seg_blocks ? kb + seg_blocks : kblocks;
-                // a later segment adds to what the one before it has written
-                if (MODE == kWgrad && !first && elect_one()) bulk_wait<0>();
-                const int acc = accs.index();
-                // after a wait that ran out the values are undefined, but the warps
-                // stay in step and the accumulator is handed back
-                if (!__all_sync(0xffffffffu, mbar_wait(acc_full0 + 8 * acc, accs.parity()))) {
+            // after a wait that ran out the values are undefined, but the warps stay in
+            // step and the accumulator is handed back
+            const auto wait_full = [&]() {
+                if (!__all_sync(0xffffffffu, mbar_wait(acc_full0 + 8 * (lt & 1), (lt >> 1) & 1))) {
                     if (lane == 0) *abort_flag = 1;
                     ok = MODE == kFc1;  // (a pair leaves at the next tile id)
                 }
-                accs.next(kblocks > seg_blocks);
                 tc_fence_after();
-                const uint32_t tbase = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(acc * TILE_N);
-                if (kChunk * set >= width) {  // no columns for this warp
-                    if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
-                    continue;
-                }
-#pragma unroll 1
-                for (int c = kChunk * set; c < width; c += kStep) {
-                    uint32_t v[kChunk];
-                    if constexpr (MODE == kMm || MODE == kDgrad) {
-                        tmem_load_16x32(tbase + c, v);  // lanes 0 - 15 and 16 - 31 of the quarter
-                        tmem_load_16x32(tbase + (16u << 16) + c, v + 16);
-                    } else if constexpr (MODE == kFc1) {
-                        tmem_load16(tbase + c, v);
-                    } else {
-                        tmem_load32(tbase + c, v);
-                    }
-                    tmem_wait_ld();
-                    if constexpr (LONG) {
-                        const uint32_t total = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)((acc ^ 1) * TILE_N);
-                        if (!first) {
-                            uint32_t before[kChunk];
-                            tmem_load32(total + c, before);
-                            tmem_wait_ld();
+            };
+            const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+            wait_full();
+            if constexpr (SUMS) {
+                if (kblocks > kSegBlocks) {  // this warp's columns of the segments, added up
+                    constexpr int kChunks = TILE_N / kStep;
+                    uint32_t total[kChunks][kChunk];
+                    uint32_t from = lanes + (uint32_t)((lt & 1) * TILE_N + kChunk * set);
 #pragma unroll
-                            for (int i = 0; i < kChunk; ++i)
-                                v[i] = __float_as_uint(__fadd_rn(__uint_as_float(before[i]), __uint_as_float(v[i])));
-                        }
-                        if (kb < kblocks) {
-                            tmem_store32(total + c, v);
-                            tmem_wait_st();
-                        }
-                    }
-                    if (c + kStep >= width) {
+                    for (int j = 0; j < kChunks; ++j) tmem_load32(from + kStep * j, total[j]);
+                    tmem_wait_ld();
+#pragma unroll 1
+                    for (int left = kblocks - kSegBlocks; left > 0 && ok; left -= kSegBlocks) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
-                    }
-                    if (LONG && kb < kblocks) continue;
-                    if (kblocks == 0) {  // nothing was accumulated
+                        if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * (lt & 1));
+                        ++lt;
+                        wait_full();
+                        from = lanes + (uint32_t)((lt & 1) * TILE_N + kChunk * set);
 #pragma unroll
-                        for (int i = 0; i < kChunk; ++i) v[i] = 0u;
-                    }
-                    if constexpr (MODE == kFc1) {
-                        const auto pair_sync = [&]() {
-                            asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
-                        };
-                        pair_sync();  // the previous chunk has been read
+                        for (int j = 0; j < 2 * kChunks; ++j) {  // (16 columns: 32 at a time spill)
+                            uint32_t v[16];
+                            tmem_load16(from + kStep * (j / 2) + 16 * (j % 2), v);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            stg_pair[i * STG_ROW_FC1 + 32 * (quarter & 1) + lane] = __uint_as_float(v[i]);
-                        pair_sync();
-                        // four lanes per row, 8 features each
-                        const int tk = 8 * (quarter & 1) + (lane >> 2), part = lane & 3;
-                        const float *src = stg_pair + tk * STG_ROW_FC1 + 8 * part;
-                        float g[8], u[8];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float4 a = lds128(src + 4 * i), b = lds128(src + 32 + 4 * i);
-                            g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
-                            u[4 * i] = b.x, u[4 * i + 1] = b.y, u[4 * i + 2] = b.z, u[4 * i + 3] = b.w;
-                        }
-                        const int n = p.features;
-                        const int col = t.m0 + 64 * (int)rank + 32 * (quarter >> 1) + 8 * part;
-                        const bool in = c + tk < t.cnt && col < n;  // (n is a multiple of 8)
-                        const int64_t row = (int64_t)t.r0 + t.n0 + c + tk;
-                        if (p.q != nullptr) {
-                            // the row's four lanes hold its 32-column block
-                            float mg = ckpt8::finite_amax<8>(g), mu = ckpt8::finite_amax<8>(u);
-#pragma unroll
-                            for (int o = 1; o < 4; o <<= 1) {
-                                mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-                                mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
-                            }
-                            const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
-                            if (in) {
-                                using St8 = swiglu::St<8, swiglu::kStStream>;
-                                uint32_t q[2];
-                                uint8_t *qr = p.q + row * 2 * n + col;
-                                ckpt8::encode<8>(g, ckpt8::encode_factor(cg), q);
-                                St8::run(qr, q);
-                                ckpt8::encode<8>(u, ckpt8::encode_factor(cu), q);
-                                St8::run(qr + n, q);
-                                if (part == 0) {
-                                    const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
-                                    uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
-                                    sr[0] = (uint8_t)cg;
-                                    sr[nb] = (uint8_t)cu;
-                                }
+                            for (int i = 0; i < 16; ++i) {
+                                uint32_t &sum = total[j / 2][16 * (j % 2) + i];
+                                sum = __float_as_uint(__fadd_rn(__uint_as_float(sum), __uint_as_float(v[i])));
                             }
                         }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * (lt & 1));
+                    ++lt;
+                    // (with the accumulator kept until it is written: 6 % slower over 2048 rows)
+#pragma unroll
+                    for (int j = 0; j < kChunks; ++j) put_weights(t, total[j], kChunk * set + kStep * j);
+                    continue;
+                }
+            }
+            const int acc = lt & 1;
+            ++lt;
+            const uint32_t tbase = lanes + (uint32_t)(acc * TILE_N);
+            if (kChunk * set >= width) {  // no columns for this warp
+                if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
+                continue;
+            }
+#pragma unroll 1
+            for (int c = kChunk * set; c < width; c += kStep) {
+                uint32_t v[kChunk];
+                if constexpr (MODE == kMm || MODE == kDgrad) {
+                    tmem_load_16x32(tbase + c, v);  // lanes 0 - 15 and 16 - 31 of the quarter
+                    tmem_load_16x32(tbase + (16u << 16) + c, v + 16);
+                } else if constexpr (MODE == kFc1) {
+                    tmem_load16(tbase + c, v);
+                } else {
+                    tmem_load32(tbase + c, v);
+                }
+                tmem_wait_ld();
+                if (c + kStep >= width) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader0 + 8 * acc);
+                }
+                if (kblocks == 0) {  // nothing was accumulated
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) v[i] = 0u;
+                }
+                if constexpr (MODE == kFc1) {
+                    const auto pair_sync = [&]() {
+                        asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
+                    };
+                    pair_sync();  // the previous chunk has been read
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        stg_pair[i * STG_ROW_FC1 + 32 * (quarter & 1) + lane] = __uint_as_float(v[i]);
+                    pair_sync();
+                    // four lanes per row, 8 features each
+                    const int tk = 8 * (quarter & 1) + (lane >> 2), part = lane & 3;
+                    const float *src = stg_pair + tk * STG_ROW_FC1 + 8 * part;
+                    float g[8], u[8];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 a = lds128(src + 4 * i), b = lds128(src + 32 + 4 * i);
+                        g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
+                        u[4 * i] = b.x, u[4 * i + 1] = b.y, u[4 * i + 2] = b.z, u[4 * i + 3] = b.w;
+                    }
+                    const int n = p.features;
+                    const int col = t.m0 + 64 * (int)rank + 32 * (quarter >> 1) + 8 * part;
+                    const bool in = c + tk < t.cnt && col < n;  // (n is a multiple of 8)
+                    const int64_t row = (int64_t)t.r0 + t.n0 + c + tk;
+                    if (p.q != nullptr) {
+                        // the row's four lanes hold its 32-column block
+                        float mg = ckpt8::finite_amax<8>(g), mu = ckpt8::finite_amax<8>(u);
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) {
+                            mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+                            mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+                        }
+                        const uint32_t cg = ckpt8::scale_code(mg), cu = ckpt8::scale_code(mu);
                         if (in) {
-                            uint32_t o[4];
-                            if (p.fc1 != nullptr) {
-                                __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
-                                swiglu::store_pack<swiglu::BF16, 8>(o, g);
-                                store16(fr, o[0], o[1], o[2], o[3]);
-                                swiglu::store_pack<swiglu::BF16, 8>(o, u);
-                                store16(fr + n, o[0], o[1], o[2], o[3]);
-                            }
-                            const float w = p.probs != nullptr && t.group != p.groups ? p.probs[row] : 1.0f;
-                            activate(g, u, w, o);
-                            store16(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, o[0], o[1], o[2], o[3]);
-                        }
-                    } else if constexpr (MODE == kWgrad) {
-                        // a lane is a row of dW; stores beyond its rows and columns
-                        // are cut off by the tensor map
-                        const int row0 = t.m0 + 128 * (int)rank + 32 * quarter;
-                        const int swz = (lane >> 1) & 3;
-                        if (p.f32_out) {
-                            const bool add = p.accumulate || !first;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                free_buffer();
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    *reinterpret_cast<uint4 *>(to + lane * 64 + ((i ^ swz) << 4)) =
-                                        make_uint4(v[16 * h + 4 * i], v[16 * h + 4 * i + 1], v[16 * h + 4 * i + 2],
-                                                   v[16 * h + 4 * i + 3]);
-                                fence_async_shared();
-                                __syncwarp();
-                                const bool in = row0 < p.features && t.n0 + c + 16 * h < p.cols;
-                                if (elect_one()) {
-                                    if (in && add)
-                                        tma_add_3d(&p.c, smem_addr(to), t.n0 + c + 16 * h, row0, t.group);
-                                    else if (in)
-                                        tma_store_3d(&p.c, smem_addr(to), t.n0 + c + 16 * h, row0, t.group);
-                                    bulk_commit();
-                                }
-                            }
-                        } else {
-                            free_buffer();
-                            uint32_t w[16];
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2)
-                                swiglu::BF16::put2(w, i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<uint4 *>(to + lane * 64 + ((i ^ swz) << 4)) =
-                                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                            fence_async_shared();
-                            __syncwarp();
-                            if (elect_one()) {
-                                if (row0 < p.features && t.n0 + c < p.cols)
-                                    tma_store_3d(&p.c, smem_addr(to), t.n0 + c, row0, t.group);
-                                bulk_commit();
+                            using St8 = swiglu::St<8, swiglu::kStStream>;
+                            uint32_t q[2];
+                            uint8_t *qr = p.q + row * 2 * n + col;
+                            ckpt8::encode<8>(g, ckpt8::encode_factor(cg), q);
+                            St8::run(qr, q);
+                            ckpt8::encode<8>(u, ckpt8::encode_factor(cu), q);
+                            St8::run(qr + n, q);
+                            if (part == 0) {
+                                const int nb = (n + ckpt8::kBlock - 1) / ckpt8::kBlock;
+                                uint8_t *sr = p.scales + row * 2 * nb + col / ckpt8::kBlock;
+                                sr[0] = (uint8_t)cg;
+                                sr[nb] = (uint8_t)cu;
                             }
                         }
-                    } else {
-                        // transposed on the way to shared memory: row r of the buffer
-                        // is row c + r of the tile, its 16-byte pieces 8 features each
-                        free_buffer();
-                        const uint32_t at = smem_addr(to) + (lane & 7) * 64 +
-                                            (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // 8 rows each
-                            uint32_t w[4];
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {  // features 8 m ..
-                                const int r = 16 * (m >> 1) + 4 * j + 2 * (m & 1);
-                                uint32_t two[1];
-                                swiglu::BF16::put2(two, 0, __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
-                                w[m] = two[0];
-                            }
-                            stmatrix_x4_trans(at + j * 8 * 64, w[0], w[1], w[2], w[3]);
+                    }
+                    if (in) {
+                        uint32_t o[4];
+                        if (p.fc1 != nullptr) {
+                            __nv_bfloat16 *fr = p.fc1 + row * 2 * n + col;
+                            swiglu::store_pack<swiglu::BF16, 8>(o, g);
+                            store16(fr, o[0], o[1], o[2], o[3]);
+                            swiglu::store_pack<swiglu::BF16, 8>(o, u);
+                            store16(fr + n, o[0], o[1], o[2], o[3]);
                         }
-                        const int col = t.m0 + 128 * (int)rank + 32 * quarter;
-                        const int row = t.r0 + t.n0 + c;
-                        const int live = t.cnt - c;
-                        if (live >= 32) {
-                            fence_async_shared();
-                            __syncwarp();
-                            if (elect_one()) {
-                                if (col < p.features) tma_store_2d(&p.c, smem_addr(to), col, row);
-                                bulk_commit();
-                            }
-                        } else {  // the rows after these are another group's
-                            __syncwarp();
-                            const int f = col + 8 * (lane & 3);
+                        const float w = p.probs != nullptr && t.group != p.groups ? p.probs[row] : 1.0f;
+                        activate(g, u, w, o);
+                        store16(static_cast<__nv_bfloat16 *>(p.out) + row * n + col, o[0], o[1], o[2], o[3]);
+                    }
+                } else if constexpr (MODE == kWgrad) {
+                    put_weights(t, v, c);
+                } else {
+                    // transposed on the way to shared memory: row r of the buffer
+                    // is row c + r of the tile, its 16-byte pieces 8 features each
+                    free_buffer();
+                    const uint32_t at = smem_addr(to) + (lane & 7) * 64 +
+                                        (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int r = 8 * i + (lane >> 2);
-                                const uint4 w = *reinterpret_cast<const uint4 *>(
-                                    to + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-                                if (r < live && f < p.features)
-                                    store16(static_cast<__nv_bfloat16 *>(p.out) + (int64_t)(row + r) * p.features + f,
-                                            w.x, w.y, w.z, w.w);
-                            }
+                    for (int j = 0; j < 4; ++j) {  // 8 rows each
+                        uint32_t w[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {  // features 8 m ..
+                            const int r = 16 * (m >> 1) + 4 * j + 2 * (m & 1);
+                            uint32_t two[1];
+                            swiglu::BF16::put2(two, 0, __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
+                            w[m] = two[0];
+                        }
+                        stmatrix_x4_trans(at + j * 8 * 64, w[0], w[1], w[2], w[3]);
+                    }
+                    const int col = t.m0 + 128 * (int)rank + 32 * quarter;
+                    const int row = t.r0 + t.n0 + c;
+                    const int live = t.cnt - c;
+                    if (live >= 32) {
+                        fence_async_shared();
+                        __syncwarp();
+                        if (elect_one()) {
+                            if (col < p.features) tma_store_2d(&p.c, smem_addr(to), col, row);
+                            bulk_commit();
+                        }
+                    } else {  // the rows after these are another group's
+                        __syncwarp();
+                        const int f = col + 8 * (lane & 3);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 8 * i + (lane >> 2);
+                            const uint4 w = *reinterpret_cast<const uint4 *>(
+                                to + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                            if (r < live && f < p.features)
+                                store16(static_cast<__nv_bfloat16 *>(p.out) + (int64_t)(row + r) * p.features + f,
+                                        w.x, w.y, w.z, w.w);
                         }
                     }
                 }
-            } while (kb < kblocks);
+            }
         }
         if (elect_one()) bulk_wait<0>();  // the stores, before their shared memory goes
     }
@@ -1102,7 +1102,7 @@ __device__ __forceinline__ void join_rows(const Params &p, const Tile &t, uint32
     }
 }
 
-template <int MODE, int NT>
+template <int MODE, int NT, bool SUMS = false>
 __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(const __grid_constant__ Params p) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -1116,7 +1116,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
     const uint32_t landed = acc_full + 8, zeroed = acc_full + 16;  // of a group's last block (kWgrad)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + 16 * kStages + 24);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(state + 16 * kStages + 28);
-    static_assert(16 * kStages + 32 <= STATE_BYTES, "barriers and state fit their region");
+    // SUMS: two accumulators in turn
+    constexpr int kSegBlocks = SUMS ? kSegmentRows / BK : INT_MAX;
+    constexpr int kTmem = SUMS ? 2 * NT : NT;
+    const auto full_of = [&](int a) { return SUMS && a != 0 ? acc_full + 32 : acc_full; };
+    const auto empty_of = [&](int a) { return acc_full + 40 + 8 * a; };
+    static_assert(16 * kStages + 56 <= STATE_BYTES, "barriers and state fit their region");
     int *starts = reinterpret_cast<int *>(state + STATE_BYTES);
     int *base = starts + kMaxGroups + 2;
     constexpr bool kAMn = MODE == kDgrad || MODE == kWgrad, kBMn = MODE == kWgrad;
@@ -1132,6 +1137,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
         mbar_init(acc_full, 1);
         mbar_init(landed, 1);
         mbar_init(zeroed, 1);
+        if (SUMS) {
+            mbar_init(full_of(1), 1);
+            mbar_init(empty_of(0), 4);
+            mbar_init(empty_of(1), 4);
+        }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
@@ -1139,7 +1149,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
-                     "r"(NT)
+                     "r"(kTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -1209,8 +1219,17 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
         }
     } else if (warp == 1 && kb1 > kb0 && elect_one()) {
         const uint32_t idesc = instr_desc(kAMn, kBMn, 128, width);
+        int seg = 0;
         for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
             const int s = it % kStages;
+            if (SUMS && it != 0 && it % kSegBlocks == 0) {
+                mma_commit(full_of(seg & 1));
+                ++seg;
+                if (!mbar_wait(empty_of(seg & 1), ((seg >> 1) & 1) ^ 1)) {
+                    *abort_flag = 1;
+                    break;
+                }
+            }
             if (!(last_rows != 0 && kb == kb1 - 1 ? mbar_wait(zeroed, 0)
                                                   : mbar_wait(full0 + 8 * s, (it / kStages) & 1))) {
                 *abort_flag = 1;
@@ -1224,40 +1243,82 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
                                         : smem_desc_128b(sa + kk * UMMA_K * 2);
                 const uint64_t b = kBMn ? smem_desc_128b(sb + kk * UMMA_K * 128, A_BYTES / 2)
                                         : smem_desc_128b(sb + kk * UMMA_K * 2);
-                mma_bf16(tmem, a, b, idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
+                const bool first = (SUMS ? it % kSegBlocks == 0 : kb == kb0) && kk == 0;
+                mma_bf16(SUMS ? tmem + (uint32_t)((seg & 1) * NT) : tmem, a, b, idesc, first ? 0u : 1u);
             }
             mma_commit(empty0 + 8 * s);
         }
-        mma_commit(acc_full);
+        mma_commit(full_of(seg & 1));
     } else if (warp >= 2 && kb1 > kb0) {
         // this CTA's partial sums, from tensor memory to [row][lane]; every load
         // of the ring has been consumed by then
         const int quarter = warp & 3;
         float *part = reinterpret_cast<float *>(smem);
-        if (MODE == kWgrad && last_rows != 0 && warp == 2) {
-            // zero the next group's rows in the last block
-            if (!__all_sync(0xffffffffu, mbar_wait(landed, 0)) && lane == 0) *abort_flag = 1;
-            unsigned char *stage = smem + (kb1 - 1 - kb0) % kStages * kStage;
-            for (int i = lane; i < (BK - last_rows) * 8; i += 32) {
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+        const auto zero_next = [&]() {  // the next group's rows in the last block
+            if (MODE == kWgrad && last_rows != 0 && warp == 2) {
+                if (!__all_sync(0xffffffffu, mbar_wait(landed, 0)) && lane == 0) *abort_flag = 1;
+                unsigned char *stage = smem + (kb1 - 1 - kb0) % kStages * kStage;
+                for (int i = lane; i < (BK - last_rows) * 8; i += 32) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    *reinterpret_cast<uint4 *>(stage + b * (A_BYTES / 2) + last_rows * 128 + i * 16) =
-                        make_uint4(0, 0, 0, 0);
+                    for (int b = 0; b < 4; ++b)
+                        *reinterpret_cast<uint4 *>(stage + b * (A_BYTES / 2) + last_rows * 128 + i * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(zeroed);
             }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(zeroed);
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(acc_full, 0)) && lane == 0) *abort_flag = 1;
-        tc_fence_after();
+        };
+        if constexpr (SUMS) {
+            constexpr int kChunk = 16;
+            float total[NT / kChunk][kChunk] = {};
+            const int segs = (kb1 - kb0 + kSegBlocks - 1) / kSegBlocks;
 #pragma unroll 1
-        for (int c = 0; c < width; c += 32) {
-            uint32_t v[32];
-            tmem_load32(tmem + ((uint32_t)(32 * quarter) << 16) + c, v);
-            tmem_wait_ld();
+            for (int seg = 0; seg < segs; ++seg) {
+                // (not sooner: the last block's loads wait for the segments before)
+                if (seg + 1 == segs) zero_next();
+                if (!__all_sync(0xffffffffu, mbar_wait(full_of(seg & 1), (seg >> 1) & 1))) {
+                    if (lane == 0) *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (c + i < width) part[(c + i) * kPartialRow + 32 * quarter + lane] = __uint_as_float(v[i]);
+                for (int j = 0; j < NT / kChunk; ++j) {
+                    if (kChunk * j < width) {
+                        uint32_t v[kChunk];
+                        tmem_load16(lanes + (uint32_t)((seg & 1) * NT + kChunk * j), v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i)
+                            total[j][i] = __fadd_rn(total[j][i], __uint_as_float(v[i]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty_of(seg & 1));
+            }
+#pragma unroll
+            for (int j = 0; j < NT / kChunk; ++j) {
+                if (kChunk * j < width) {  // (width is a multiple of 16)
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i)
+                        part[(kChunk * j + i) * kPartialRow + 32 * quarter + lane] = total[j][i];
+                }
+            }
+        } else {
+            zero_next();
+            if (!__all_sync(0xffffffffu, mbar_wait(acc_full, 0)) && lane == 0) *abort_flag = 1;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < width; c += 32) {
+                uint32_t v[32];
+                tmem_load32(lanes + c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c + i < width) part[(c + i) * kPartialRow + 32 * quarter + lane] = __uint_as_float(v[i]);
+            }
         }
     }
     tc_fence_before();
@@ -1287,7 +1348,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) grouped_mm_split_kernel(cons
     if (size > 1) cluster_sync_read();  // no CTA leaves while another may still read its sums
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NT) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
     }
 }
 
@@ -1360,7 +1421,7 @@ constexpr int kSms = 152;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // One cluster per tile, of which there are `clusters` at most.
-template <int MODE, bool LONG = false>
+template <int MODE, bool SUMS = false>
 swiglu_status_t launch_pairs(const Params &p, int64_t clusters, swiglu_stream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1369,11 +1430,11 @@ swiglu_status_t launch_pairs(const Params &p, int64_t clusters, swiglu_stream_t 
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (!(dev >= 0 && dev < kMaxDevices && attr_set[dev].load())) {
-        e = cudaFuncSetAttribute(grouped_mm_kernel<MODE, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        e = cudaFuncSetAttribute(grouped_mm_kernel<MODE, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
         if (e != cudaSuccess) return moe::cuda_fail(e);
         if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true);
     }
-    e = moe::launch(grouped_mm_kernel<MODE, LONG>, dim3((unsigned)(2 * clusters)), kPairThreads, SMEM_BYTES,
+    e = moe::launch(grouped_mm_kernel<MODE, SUMS>, dim3((unsigned)(2 * clusters)), kPairThreads, SMEM_BYTES,
                     stream, 0, p);
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
@@ -1386,7 +1447,7 @@ int64_t most_tiles(int64_t rows, int64_t groups, int64_t features, int tile_f, i
     return (rows + (tn - 1) * g) / tn * ((features + tile_f - 1) / tile_f);
 }
 
-template <int MODE, int NT>
+template <int MODE, int NT, bool SUMS = false>
 swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_stream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1394,13 +1455,13 @@ swiglu_status_t launch_split(const Params &p, int64_t tiles, int size, swiglu_st
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (!(dev >= 0 && dev < kMaxDevices && attr_set[dev].load())) {
-        e = cudaFuncSetAttribute(grouped_mm_split_kernel<MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(grouped_mm_split_kernel<MODE, NT, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSplitSmem<NT>);
         if (e != cudaSuccess) return moe::cuda_fail(e);
         if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true);
     }
-    e = moe::launch(grouped_mm_split_kernel<MODE, NT>, dim3((unsigned)(tiles * size)), kSplitThreads, kSplitSmem<NT>,
-                    stream, size, p);
+    e = moe::launch(grouped_mm_split_kernel<MODE, NT, SUMS>, dim3((unsigned)(tiles * size)), kSplitThreads,
+                    kSplitSmem<NT>, stream, size, p);
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);
 }
 
@@ -1420,10 +1481,9 @@ struct Plan {
 
 // `same` groups of `rows_per` rows (kWgrad: dW's rows, N) by `features`; pair_f
 // and split_f: features of a tile, nt: rows of a tile of the split kernel, most: its
-// tiles at most; least_size: the fewest slices a sum may be cut into (pairs cut it
-// themselves).
+// tiles at most.
 Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int split_f, int nt, int64_t most,
-          int64_t kblocks, int64_t least_size = 1) {
+          int64_t kblocks) {
     const int64_t pair_n = rows_per < TILE_N ? ceil_div(rows_per, 32) * 32 : TILE_N;
     const int64_t pair_tiles = same * ceil_div(rows_per, TILE_N) * ceil_div(features, pair_f);
     const int64_t pair_depth = kblocks * (A_BYTES + pair_n * BK) * 100 / 8955;
@@ -1433,7 +1493,6 @@ Plan plan(int64_t same, int64_t rows_per, int64_t features, int pair_f, int spli
     const int64_t split_tiles = same * ceil_div(rows_per, nt) * ceil_div(features, split_f);
     const int64_t beyond = most > split_tiles ? most - split_tiles : 0;
     for (int size = 1; size <= 8 && (size == 1 || 2 * size <= kblocks); size *= 2) {
-        if (size < least_size) continue;
         const int64_t ctas = split_tiles * size;
         const int64_t bytes = ceil_div(kblocks, size) * (A_BYTES + split_n * BK * 2);
         const int64_t time = (ctas <= kSms ? bytes * 10 / 896 : ceil_div(ctas, kSms) * bytes * 10 / 1066) +
@@ -1466,10 +1525,9 @@ int64_t wgrad_split_tiles(int64_t groups, int64_t N, int64_t K) {
     return groups * ceil_div(N, 128) * ceil_div(K, kSplitF<kWgrad>);
 }
 
-// A sum's slices stay within a segment.
-Plan plan_wgrad(int64_t rows, int64_t groups, int64_t N, int64_t K, bool f32) {
+Plan plan_wgrad(int64_t rows, int64_t groups, int64_t N, int64_t K) {
     return plan(groups, N, K, 256, kSplitF<kWgrad>, 128, wgrad_split_tiles(groups, N, K),
-                ceil_div(ceil_div(rows, groups), BK), ceil_div(rows, f32 ? kSegmentRows : kLongRows));
+                ceil_div(ceil_div(rows, groups), BK));
 }
 
 // Launch a product over rows.
@@ -1654,13 +1712,17 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
     p.accumulate = accumulate != 0;
     // Pairs: M is dW's rows, N its columns.  Split: the other way round, so that the
     // lanes run along dW's rows.
-    const int size = plan_wgrad(rows, groups, N, K, p.f32_out).size;
+    const int size = plan_wgrad(rows, groups, N, K).size;
+    // where one group had all rows: does a sum have several segments?
+    const bool sums = rows > (int64_t)(p.f32_out ? kSegmentRows : kLongRows) * (size > 0 ? size : 1);
     if (size > 0) {
         if (!map2(enc, &p.a, x, K, rows, BK) || !map2(enc, &p.b[0], dy, N, rows, BK))
             return moe::cuda_fail(cudaErrorInvalidValue);
         p.features = (int)K;
         p.cols = (int)N;
-        return launch_split<kWgrad, 128>(p, wgrad_split_tiles(groups, N, K), size, stream);
+        const int64_t tiles = wgrad_split_tiles(groups, N, K);
+        return sums ? launch_split<kWgrad, 128, true>(p, tiles, size, stream)
+                    : launch_split<kWgrad, 128>(p, tiles, size, stream);
     }
     if (!map2(enc, &p.a, dy, N, rows, BK) || !map2(enc, &p.b[0], x, K, rows, BK) ||
         !out_map(enc, &p.c, dw, eb, K, N, groups))
@@ -1670,8 +1732,7 @@ swiglu_status_t swiglu_grouped_mm_wgrad(const void *dy, const void *x, const int
             return moe::cuda_fail(cudaErrorInvalidValue);
     p.features = (int)N;
     p.cols = (int)K;
-    if (!p.f32_out && rows > kLongRows) return launch_pairs<kWgrad, true>(p, pairs, stream);
-    return launch_pairs<kWgrad>(p, pairs, stream);
+    return sums ? launch_pairs<kWgrad, true>(p, pairs, stream) : launch_pairs<kWgrad>(p, pairs, stream);
 }
 
 swiglu_status_t swiglu_grouped_slices(swiglu_grouped_product_t product, int64_t rows, int64_t groups, int64_t N,
@@ -1692,7 +1753,7 @@ swiglu_status_t swiglu_grouped_slices(swiglu_grouped_product_t product, int64_t 
         case SWIGLU_GROUPED_WGRAD:
             if (dw_dtype != SWIGLU_BF16 && dw_dtype != SWIGLU_F32) return SWIGLU_ERR_DTYPE;
             if (rows > SWIGLU_GROUPED_MAX_ROWS_WGRAD) return SWIGLU_ERR_SHAPE;
-            *slices = plan_wgrad(rows, groups, N, K, dw_dtype == SWIGLU_F32).size;
+            *slices = plan_wgrad(rows, groups, N, K).size;
             return SWIGLU_OK;
     }
     return SWIGLU_ERR_SHAPE;

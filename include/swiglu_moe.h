@@ -96,7 +96,7 @@ swiglu_status_t swiglu_ckpt8_bwd(const void *dy, const void *q, const void *scal
  * every result rounded once; contiguous tensors, 16-byte aligned pointers).
  * The tensor cores truncate the running sum every 16 terms: a sum of D terms is
  * within D 2^-27 of the sum of their absolute values.  D is the depth of a
- * product over rows; weight gradients add up sums of at most 4096 (fp32 dW) or
+ * product over rows; weight gradients add up sums of at most 512 (fp32 dW) or
  * 131,072 rows (bf16 dW) with rounded fp32 additions.
  * For each row t of group e:
  *

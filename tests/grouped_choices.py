@@ -20,9 +20,10 @@ CASES = [
     ("wgrad", BF16, 0, 1500, 5, 1288, 1288), ("wgrad", BF16, 0, 700, 5, 776, 1032),
     ("wgrad", BF16, 1, 300, 5, 520, 1160), ("wgrad", BF16, 2, 1925, 5, 72, 72), ("wgrad", BF16, 4, 2600, 4, 136, 72),
     ("wgrad", BF16, 8, 6000, 4, 136, 264),
-    ("wgrad", F32, 0, 1500, 5, 1288, 1288), ("wgrad", F32, 0, 9500, 3, 1032, 1288),
-    ("wgrad", F32, 1, 300, 5, 520, 1160), ("wgrad", F32, 2, 4197, 7, 8, 1304), ("wgrad", F32, 4, 2600, 4, 136, 72),
-    ("wgrad", F32, 8, 6000, 4, 136, 264),
+    ("wgrad", F32, 0, 500, 5, 1032, 1288), ("wgrad", F32, 0, 1500, 5, 1288, 1288),
+    ("wgrad", F32, 0, 7000, 3, 1288, 1288), ("wgrad", F32, 1, 300, 5, 520, 1160), ("wgrad", F32, 1, 4197, 7, 8, 1304),
+    ("wgrad", F32, 2, 1000, 3, 72, 72), ("wgrad", F32, 2, 1925, 5, 72, 72), ("wgrad", F32, 4, 2000, 3, 136, 136),
+    ("wgrad", F32, 4, 2600, 4, 136, 72), ("wgrad", F32, 8, 3900, 3, 136, 264), ("wgrad", F32, 8, 6000, 4, 136, 264),
 ]
 
 

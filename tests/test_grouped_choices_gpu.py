@@ -258,14 +258,13 @@ def test_bf16_weight_gradients_over_many_rows(sw):
         assert torch.equal(_bits(got[e]), _bits(want.bfloat16())), f"group of {c} rows"
 
 
-@pytest.mark.parametrize("N,K,slices", [(2056, 2048, 0), (128, 136, 8)])
-def test_bf16_weight_gradients_keep_their_precision(sw, N, K, slices):
-    """600,000 rows of one sign.  Each step of 16 rows truncates the running sum by less
+@pytest.mark.parametrize("rows,N,K,slices", [(600_000, 2056, 2048, 0), (600_000, 128, 136, 8), (1_200_000, 72, 72, 8)])
+def test_bf16_weight_gradients_keep_their_precision(sw, rows, N, K, slices):
+    """Many rows of one sign.  Each step of 16 rows truncates the running sum by less
     than 2^-23 of it, so 131,072 rows lose at most 2^13 2^-23 = 2^-10; with the rounding
     to bf16 (8 significant bits: 2^-8) and of the additions every value is within 2^-8 +
-    2^-10 + 2^-20.  One running sum would lose 3.8e-3 on average."""
+    2^-10 + 2^-20.  One running sum of 600,000 would lose 3.8e-3 on average."""
     g = torch.Generator(device="cuda").manual_seed(4)
-    rows = 600_000
     assert sw.grouped_slices("wgrad", rows, 1, N, K) == slices
     x = torch.randn(rows, K, generator=g, device="cuda").bfloat16().abs()
     dy = torch.randn(rows, N, generator=g, device="cuda").bfloat16().abs()
@@ -275,3 +274,23 @@ def test_bf16_weight_gradients_keep_their_precision(sw, N, K, slices):
     for r in range(0, rows, 65536):
         want += dy[r:r + 65536, some].double().T @ x[r:r + 65536].double()
     assert float(((got.double() - want).abs() / want).max()) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("counts,N,K,slices", [([13_000, 0, 300, 4000], 1288, 1544, 0), ([5200, 40], 1032, 264, 4),
+                                               ([13_000], 136, 72, 8)])
+def test_fp32_weight_gradients_keep_their_precision(sw, counts, N, K, slices):
+    """Rows of one sign, in fp32.  A sum of 512 rows takes 32 steps, each of which truncates
+    it by less than 2^-23 of it; the sums are added with rounded additions, one per 512
+    rows (and per slice, and one to what dW holds)."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rows, E, ends = sum(counts) + 9, len(counts), _ends(counts)
+    assert sw.grouped_slices("wgrad", rows, E, N, K, torch.float32) == slices
+    x = torch.randn(rows, K, generator=g, device="cuda").bfloat16().abs()
+    dy = torch.randn(rows, N, generator=g, device="cuda").bfloat16().abs()
+    want = R.wgrad(dy, x, ends, E)[0]
+    tol = 32 * 2.0 ** -23 + (-(-max(counts) // 512) + 9) * 2.0 ** -24
+    dw = sw.swiglu_grouped_mm_wgrad(dy, x, ends, dtype=torch.float32)
+    assert bool(((dw.double() - want).abs() <= tol * want).all())
+    start = torch.randn(E, N, K, generator=g, device="cuda").abs()
+    more = sw.swiglu_grouped_mm_wgrad(dy, x, ends, dw=start.clone(), accumulate=True)
+    assert bool(((more.double() - start.double() - want).abs() <= tol * (want + start.double())).all())
