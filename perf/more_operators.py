@@ -163,8 +163,14 @@ def _run_own(s):
         q, scales = sw.swiglu_mx4_quantize(s["x"])
         return sw.swiglu_mx4_dequantize(q, scales, c["n"], dtype=s["x"].dtype)
     if op == "mm":
-        return sw.swiglu_mx4_mm_fwd(*s["x"], *s["w"])
-    return sw.swiglu_mx4_mlp_fwd(s["x"], *s["w1"], *s["w2"])
+        return sw.swiglu_mx4_mm_fwd(*_as_bytes(*s["x"]), *_as_bytes(*s["w"]))
+    return sw.swiglu_mx4_mlp_fwd(s["x"], *_as_bytes(*s["w1"]), *_as_bytes(*s["w2"]))
+
+
+def _as_bytes(q, scales):
+    """The package's operators take codes as bytes: prepare() keeps them in 64 bits, so
+    this conversion is a part of the pass."""
+    return q.to(torch.uint8), scales
 
 
 def _norm(x, w, b):
@@ -190,7 +196,7 @@ def _codes(x):
     v = torch.where(bad[..., None], 0.0, v * up[..., None])
     a = v.abs()
     code = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5))
-    return code + 8 * torch.signbit(v).to(torch.uint8), scale.to(torch.uint8)
+    return code + 8 * torch.signbit(v), scale.to(torch.uint8)
 
 
 def _quantize(x, parts=1):
