@@ -940,19 +940,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int row = m0 + 128 * (int)rank + 32 * quarter + lane;
             // the shared columns: the last 72 of the first accumulator, the first 72 of the
             // second.  A warp that has some of them (a gated one does: its gate and up
-            // columns lie 128 apart) arrives when it has read them, the others now that they
-            // are done with the tile before
+            // columns lie 128 apart) arrives when it has read them, the others once this
+            // tile's products are done, since they have read the tile before.  No warp
+            // arrives for a tile before that: its products start when every warp has arrived
+            // for the tile before, so no warp counts twice among the 16 of a tile (one that
+            // arrived without waiting would take the place of a warp that has still to read)
             const bool sharing = kGated || half != acc;
-            if (!sharing) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader);
-            }
             if (!__all_sync(0xffffffffu, wait(acc_full0 + 8 * acc, (k >> 1) & 1))) {
                 if (lane == 0) *abort_flag = 1;
                 break;
             }
             tc_fence_after();
+            const auto read = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader);
+            };
+            if (!sharing) read();
             const uint32_t base = tmem + ((uint32_t)(32 * quarter) << 16) + acc * kAccShift;
             uint32_t v[64], u[64];
             const auto load64 = [&](int col, uint32_t(&to)[64]) {
@@ -963,11 +967,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             load64(first, v);
             load64(second, u);
             tmem_wait_ld();
-            if (sharing) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_read(acc_empty_leader);
-            }
+            if (sharing) read();
             if constexpr (kGated) {
                 if (row < M) store_blocks(out, row, tn * 128 + first, v, u, wide);
             } else if constexpr (kTo == kWholePacks) {
