@@ -794,12 +794,12 @@ __global__ void __launch_bounds__(T, 1) layer_norm_bwd_kernel(const __grid_const
         ok = ok && row_arrived(bar0 + 8 * slot, parity);  // one that ran out is not waited for again
         const uint32_t at = slot0 + slot * p.slot_bytes;
         uint64_t xhat[N], h[N], s0 = 0, s1 = 0;
-        const uint64_t m = twice(mean), scale = twice(rstd);
+        const uint64_t scale = twice(rstd);
         uint32_t xw[C][WN], dw[C][WN];
         if constexpr (ANY) {
             const float x1 = shifted_packs<E>(x_row(row), at, cols, xw), dy1 = shifted_packs<E>(dy_row(row), at + half, cols, dw);
             if (t < 32) {
-                const float xhat1 = (x1 - mean) * rstd;
+                const float xhat1 = cols.single >= 0 ? (x1 - mean) * rstd : 0.0f;
                 lone[g][1][t] = fmaf(dy1, xhat1, lone[g][1][t]);
                 lone[g][2][t] += dy1;
                 const float h1 = dy1 * lone[g][0][t];
@@ -812,8 +812,10 @@ __global__ void __launch_bounds__(T, 1) layer_norm_bwd_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const uint64_t dy = pair_of<E, VEC, C>(dw, i);
+            // (columns past the row hold x = 0 and dy = 0; with a mean of 0 they add nothing,
+            // where -mean rstd may be infinite)
+            const uint64_t m = swiglu::x2(in[2 * i / VEC] ? mean : 0.0f, in[(2 * i + 1) / VEC] ? mean : 0.0f);
             xhat[i] = swiglu::mul_x2(swiglu::sub_x2(pair_of<E, VEC, C>(xw, i), m), scale);
-            // (columns past the row hold dy = 0: they add nothing)
             aw[i] = swiglu::fma_x2(dy, xhat[i], aw[i]);
             ab[i] = swiglu::add_x2(dy, ab[i]);
             h[i] = swiglu::mul_x2(dy, pair_of<P, VEC, C>(ww, i));

@@ -276,3 +276,20 @@ def test_rows_split_over_a_cluster(sw, rows, n, dtype):
     first = check_bwd(sw, dy, x, w)
     assert all(torch.equal(a, c) for a, c in zip(first, check_bwd(sw, dy, x, w)))
     assert sw.layer_norm_timeout_flag() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("rows,n", [(6, 40), (6, 500), (6, 512), (700, 513), (700, 4000), (700, 4095), (700, 4096),
+                                    (6, 5503), (90, 8193), (40, 20000), (40, 32761), (40, 32768), (3, 70000)])
+def test_backward_of_constant_rows_of_large_values(sw, rows, n, pad, dtype):
+    """xhat = 0, and dx = rstd (h - mean(h)), whether or not the threads that share a row have
+    columns past its end (mean * rstd is beyond fp32)."""
+    _, dy, w, _ = make(rows, n, dtype, seed=n, pad=pad)
+    x = torch.full((rows, n + pad), 1e33, device="cuda").to(dtype)[:, :n]
+    mean, rstd = x[:, 0].float().contiguous(), torch.full((rows,), 1e6, device="cuda")
+    dx, dw, db = sw.swiglu_layer_norm_bwd(dy, x, mean, rstd, w)
+    want = bwd64(dy, x, mean, rstd, w)
+    within(dx, want[0], want[3], dtype, "dx")
+    assert bool((dw == 0).all())
+    within(db, want[2], want[5], dtype, "db")
