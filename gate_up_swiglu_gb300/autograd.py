@@ -27,6 +27,12 @@ from . import (swiglu_gateup_bias_bwd, swiglu_gateup_bias_fwd, swiglu_gateup_bwd
 log = logging.getLogger(__name__)
 
 
+def carries_tangent(*tensors: Optional[torch.Tensor]) -> bool:
+    """Whether a forward-mode derivative runs through one of the tensors: a call that passes
+    by its autograd function would drop it without a word, the function raises."""
+    return any(t is not None and torch.autograd.forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def _bump_version(t: torch.Tensor) -> None:
     # the kernel writes through a raw pointer, which autograd cannot see
     inc = getattr(torch.autograd.graph, "increment_version", None)

@@ -27,6 +27,7 @@ from torch.autograd.function import once_differentiable
 from . import (swiglu_ckpt8_bwd, swiglu_ckpt8_fwd, swiglu_gateup_bwd, swiglu_gateup_fwd, swiglu_gateup_weighted_bwd,
                swiglu_gateup_weighted_fwd, swiglu_grouped_fc1_fwd, swiglu_grouped_mm_dgrad, swiglu_grouped_mm_fwd,
                swiglu_grouped_mm_wgrad)
+from .autograd import carries_tangent
 
 CHECKPOINTS = ("fp8", "bf16")
 
@@ -120,7 +121,8 @@ class ExpertsSwiGLU(torch.nn.Module):
     forward(x [rows, hidden], counts [E], probs=None): rows sorted by expert,
     ``counts`` the rows per expert (a CUDA integer tensor; the host does not read
     it), ``probs`` one routing weight per row.  Without gradients nothing is kept
-    of the first product (prefill and decode steps)."""
+    of the first product (prefill and decode steps).  There is no forward-mode derivative:
+    a tangent raises."""
 
     def __init__(self, experts: int, hidden: int, ffn_hidden: int, checkpoint: str = "fp8", device=None,
                  dtype=torch.bfloat16):
@@ -138,7 +140,7 @@ class ExpertsSwiGLU(torch.nn.Module):
             raise ValueError("x must be [rows, hidden] and counts hold the rows of each expert")
         ends = group_ends(counts)
         tracked = (x, self.w1, self.w2) if probs is None else (x, probs, self.w1, self.w2)
-        if torch.is_grad_enabled() and any(t.requires_grad for t in tracked):
+        if torch.is_grad_enabled() and any(t.requires_grad for t in tracked) or carries_tangent(*tracked):
             return ExpertsSwiGLUFunction.apply(x, probs, self.w1, self.w2, ends, self.checkpoint)
         p32 = None if probs is None else probs.reshape(-1).to(torch.float32).contiguous()
         y = swiglu_grouped_fc1_fwd(x.contiguous(), self.w1, ends, p32)

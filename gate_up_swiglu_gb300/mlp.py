@@ -20,6 +20,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import mx4_scales_shape, swiglu_layer_norm_bwd, swiglu_layer_norm_fwd, swiglu_mx4_quantize
+from .autograd import carries_tangent
 from .mx4 import MX4_BLOCK, SCALE_DTYPE, _mlp_fwd, _need_scale_type
 
 
@@ -49,8 +50,9 @@ class LayerNormFunction(torch.autograd.Function):
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                eps: float = 1e-5) -> torch.Tensor:
     """The layer norm over the last dimension; keeps x, mean and rstd where a gradient
-    will be asked for."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+    will be asked for.  It has no forward-mode derivative: a tangent raises."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)) or \
+            carries_tangent(x, weight, bias):
         return LayerNormFunction.apply(x, weight, bias, eps)
     return swiglu_layer_norm_fwd(x, weight, bias, eps)
 
@@ -76,8 +78,8 @@ class Mx4SwiGLU(torch.nn.Module):
     """The gated MLP (bias-free) with weights and activations in 4 bits, for serving:
     w1 [2 * ffn_hidden, hidden] with gate rows first, w2 [out, ffn_hidden] (out =
     hidden unless given), held as uint8 buffers of codes and scale bytes, which a change
-    of the module's dtype leaves alone.  It has no backward: an input that requires a
-    gradient is refused while gradients are on."""
+    of the module's dtype leaves alone.  It has no derivatives: an input that requires a
+    gradient is refused while gradients are on, and so is one with a tangent."""
 
     def __init__(self, hidden: int, ffn_hidden: int, out: int = None, device=None):
         super().__init__()
@@ -105,4 +107,6 @@ class Mx4SwiGLU(torch.nn.Module):
             raise ValueError(f"x must be [..., {self.hidden}]")
         if torch.is_grad_enabled() and x.requires_grad:
             raise NotImplementedError("the 4-bit MLP has no backward: call it under torch.no_grad()")
+        if carries_tangent(x):
+            raise NotImplementedError("the 4-bit MLP has no forward-mode derivative: call it on the primal tensor")
         return _mlp_fwd(x, self.w1_q, self.w1_scales, self.w2_q, self.w2_scales, None, None, None, torch.uint8)

@@ -151,3 +151,19 @@ def test_fp8_input_store_of_the_activation_modules(sw):
     y.backward(dy.view(30, 72))
     dx, dw, _ = sw.swiglu_ckpt8_bwd(dy.view(30, 72), q.view(30, 144), s.view(30, -1), wg.detach().float().view(-1))
     assert torch.equal(x2.grad, dx) and torch.equal(wg.grad, dw.view(30, 1).bfloat16())
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_derivatives_are_refused(sw, grad):
+    """A tangent of any input or weight raises, with gradients on and off."""
+    import torch.autograd.forward_ad as fw
+    from gate_up_swiglu_gb300.experts import ExpertsSwiGLU
+
+    x, w1, w2, p, _, counts = _inputs([5, 3], 0, 64, 32, 0)
+    layer = ExpertsSwiGLU(2, 64, 32, device="cuda").requires_grad_(False)
+    want = layer(x, counts, p)
+    with fw.dual_level(), torch.set_grad_enabled(grad):
+        for args in ((fw.make_dual(x, x), counts, p), (x, counts, fw.make_dual(p, p))):
+            with pytest.raises((RuntimeError, NotImplementedError), match="jvp"):
+                layer(*args)
+        assert torch.equal(layer(x, counts, p), want)

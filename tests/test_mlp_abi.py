@@ -211,6 +211,16 @@ def test_modules_refuse_wrong_shapes(sw):
         Mx4SwiGLU.from_weights(torch.zeros(10, 8), torch.zeros(8, 4))
 
 
+def test_mx4_module_refuses_tangents(sw):
+    import torch.autograd.forward_ad as fw
+    from gate_up_swiglu_gb300.mlp import Mx4SwiGLU
+
+    m, x = Mx4SwiGLU(64, 40), torch.zeros(2, 64)
+    with fw.dual_level(), torch.no_grad():
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            m(fw.make_dual(x, x))
+
+
 def test_a_torch_without_the_scale_type_keeps_the_rest(sw):
     code = """
 import torch
