@@ -30,7 +30,10 @@ log = logging.getLogger(__name__)
 def carries_tangent(*tensors: Optional[torch.Tensor]) -> bool:
     """Whether a forward-mode derivative runs through one of the tensors: a call that passes
     by its autograd function would drop it without a word, the function raises."""
-    return any(t is not None and torch.autograd.forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+    fw = torch.autograd.forward_ad
+    if getattr(fw, "_current_level", 0) < 0:  # no level is open (1 us less than to ask three tensors)
+        return False
+    return any(t is not None and fw.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _bump_version(t: torch.Tensor) -> None:
