@@ -27,8 +27,8 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
     return (uint32_t)max((int)((amax + 0x3fffffu) >> 23) - 2, 0);
 }
 
-// 2^(127 - c), exact for c <= 253.  A NaN block (c = 255) takes the factor 0:
-// finite values become zero codes (NaN and infinities are cleared by `clean`).
+// 2^(127 - c), exact for c <= 253.  A NaN block (c = 255) takes the factor 0 (which leaves
+// NaN and infinities NaN: scale_values puts zeros for the whole block).
 __device__ __forceinline__ float encode_factor(uint32_t c) {
     return c == 255 ? 0.0f : __uint_as_float((254u - c) << 23);
 }
