@@ -90,9 +90,11 @@ __device__ __forceinline__ int64_t scale_offset(int64_t tile, int64_t i, int32_t
 // A thread takes eight or sixteen neighbouring elements (a pack) of kRows rows below
 // each other, so that what it costs to find its place comes once; 32 / VEC neighbouring
 // lanes hold a block.  The index space covers the scale tiles: padded rows (whole tiles a
-// part) and padded blocks (whole chunks), so that every scale byte is written.
+// part) and padded blocks (whole chunks), so that every scale byte is written; and so every
+// thread of a CTA has a place, and all lanes of a warp take part in its shuffles.
 
 constexpr int kRows = 4;
+constexpr int kPlaces = kTileRows / kRows * (kTileBlocks * kBlock / 16);  // of a scale tile, in the longer packs
 
 struct ConvParams {
     const char *x;   // the tensor: source of quantising,
@@ -102,7 +104,6 @@ struct ConvParams {
     int64_t rows;         // a part
     int64_t padded_rows;  // a part
     int64_t stride;       // of x or y, bytes
-    int64_t units;        // packs of kRows rows, all parts
     int64_t n;
     uint64_t lo, hi;      // x's bytes, rounded inwards to 16 (see load_any)
     int32_t nb, chunks;
@@ -167,12 +168,10 @@ __global__ void __launch_bounds__(T) mx4_quantize_kernel(const __grid_constant__
     swiglu::await_previous_grid();
     swiglu::allow_next_grid();
     const int64_t unit = (int64_t)blockIdx.x * T + threadIdx.x;
-    if (unit >= p.units) return;  // whole blocks: row_units is a multiple of 4 L
     const Place at = locate(p, unit);
     const int32_t b = at.c / L;
     const int64_t col = (int64_t)at.c * VEC;
     const int left = p.n - col < VEC ? (int)(p.n - col) : VEC;  // elements of the pack inside the row
-    const uint32_t lanes = __activemask();
     uint32_t w[kRows][NW];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(T) mx4_quantize_kernel(const __grid_constant__
             m = max(m & 0xffff0000u, m << 16);
         }
 #pragma unroll
-        for (int d = 1; d < L; d *= 2) m = max(m, __shfl_xor_sync(lanes, m, d));
+        for (int d = 1; d < L; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
         const uint32_t sc = scale_byte(m);
         const bool live = at.i + r < p.rows;
         if (live && b < p.nb) {
@@ -263,13 +262,13 @@ __device__ __forceinline__ void store_element(char *dst, const uint32_t (&w)[2 *
 // that the row's end cuts (left < 8).
 template <typename E>
 __device__ __forceinline__ void store_any(char *dst, const uint32_t (&w)[2 * E::kBytes], const uint32_t (&before)[4],
-                                          uint32_t lanes, bool first, bool last, int left) {
+                                          bool first, bool last, int left) {
     constexpr int NW = 2 * E::kBytes;
     const uint32_t off = (uint32_t)(reinterpret_cast<uint64_t>(dst) & 15);
     uint32_t r[4 + NW];  // the neighbour's last 16 bytes, then the pack
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        r[k] = __shfl_up_sync(lanes, w[NW - 4 + k], 1);
+        r[k] = __shfl_up_sync(0xffffffffu, w[NW - 4 + k], 1);
         if ((threadIdx.x & 31) == 0) r[k] = before[k];
     }
 #pragma unroll
@@ -302,12 +301,10 @@ __global__ void __launch_bounds__(T) mx4_dequantize_kernel(const __grid_constant
     swiglu::await_previous_grid();
     swiglu::allow_next_grid();
     const int64_t unit = (int64_t)blockIdx.x * T + threadIdx.x;
-    if (unit >= p.units) return;
     const Place at = locate(p, unit);
     const int32_t b = at.c / L;
     const int64_t col = (int64_t)at.c * VEC;
     const int left = p.n - col < VEC ? (int)(p.n - col) : VEC;  // elements of the pack inside the row
-    const uint32_t lanes = __activemask();
     // the last eight codes of the pack to the left, for a warp's first lane (see store_any)
     const bool reach = ANY && (threadIdx.x & 31) == 0 && at.c > 0 && left > 0;
     uint32_t q[kRows][VEC / 8], sc[kRows], qb[kRows], scb[kRows];
@@ -349,7 +346,7 @@ __global__ void __launch_bounds__(T) mx4_dequantize_kernel(const __grid_constant
 #pragma unroll
                 for (int k = 0; k < 4; ++k) before[k] = all[NW - 4 + k];
             }
-            store_any<E>(dst, w, before, lanes, at.c == 0, p.n - col < 16, live ? left : 0);
+            store_any<E>(dst, w, before, at.c == 0, p.n - col < 16, live ? left : 0);
         } else if (live && left > 0) {
             swiglu::St<B, swiglu::kStStream>::run(dst, w);
         }

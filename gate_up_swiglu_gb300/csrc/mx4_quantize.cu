@@ -44,10 +44,10 @@ ConvParams params(const void *data, const void *q, const void *scales, int64_t r
 template <typename K>
 swiglu_status_t launch(K kernel, ConvParams p, int vec, int64_t parts, swiglu_stream_t stream) {
     p.row_units = p.chunks * (kTileBlocks * kBlock / vec);
-    p.units = parts * (p.padded_rows / kRows) * p.row_units;
     p.div_row = swiglu::make_fast_div((uint64_t)p.row_units);
     p.div_part = swiglu::make_fast_div((uint64_t)(p.padded_rows / kRows));
-    const int64_t ctas = (p.units + kT - 1) / kT;
+    static_assert(kPlaces % kT == 0, "no CTA is cut: a warp's shuffles have all its lanes");
+    const int64_t ctas = parts * (p.padded_rows / kRows) * p.row_units / kT;
     if (ctas > INT32_MAX) return SWIGLU_ERR_SHAPE;
     const cudaError_t e = moe::launch(kernel, dim3((unsigned)ctas), kT, 0, stream, 0, p);
     return e == cudaSuccess ? SWIGLU_OK : moe::cuda_fail(e);

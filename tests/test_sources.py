@@ -47,3 +47,9 @@ def test_a_pair_that_gave_up_stays_until_its_loads_have_landed(name, kernel_name
     part = kernel[kernel.index(roles[0]):kernel.index(roles[1])]
     assert part.count("give_up();") == sites and "*abort_flag = 1" not in part
     assert re.search(r"void settle\(\) \{[^}]*kSettleNs", open(os.path.join(CSRC, "tc_pair.cuh")).read())
+
+
+@pytest.mark.parametrize("path", sorted(glob.glob(os.path.join(CSRC, "*.cu*"))), ids=os.path.basename)
+def test_shuffles_name_their_lanes(path):
+    """No mask of the lanes that happen to be converged."""
+    assert "__activemask" not in open(path).read()
