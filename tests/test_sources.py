@@ -53,3 +53,15 @@ def test_a_pair_that_gave_up_stays_until_its_loads_have_landed(name, kernel_name
 def test_shuffles_name_their_lanes(path):
     """No mask of the lanes that happen to be converged."""
     assert "__activemask" not in open(path).read()
+
+
+def test_columns_of_an_accumulator_are_given_free_after_its_products():
+    """The 4-bit pair kernel's epilogue warps arrive for a tile once each, behind their wait for
+    the tile's products: ahead of it a warp could arrive twice for one tile, in the place of one
+    that has still to read the columns that the next tile overwrites."""
+    text = open(os.path.join(CSRC, "mx4_mm.cu")).read()
+    kernel = text[text.index("mx4_pair_kernel(const __grid_constant__"):]
+    loop = kernel[kernel.index("// ---- epilogue"):kernel.index("\n}\n")]
+    wait = loop.index("wait(acc_full0")
+    assert "(acc_empty_leader)" in loop[wait:] and "(acc_empty_leader)" not in loop[:wait]
+    assert loop.count("(acc_empty_leader)") == 1 and loop.index("if (!sharing) read();") < loop.index("if (sharing) read();")
