@@ -286,8 +286,10 @@ swiglu_status_t launch_bwd(lnorm::BwdParams p, const Plan &plan, int dev, swiglu
         e = moe::launch(lnorm::layer_norm_bwd_sums_kernel<E, P, VEC, 512>, dim3((unsigned)p.rows), 512, 0, stream, 0, p);
         if (e != cudaSuccess) return moe::cuda_fail(e);
         const int64_t tiles = (p.n + (int64_t)kTileThreads * VEC - 1) / ((int64_t)kTileThreads * VEC);
-        e = moe::launch(lnorm::layer_norm_bwd_tile_kernel<E, P, VEC, kTileThreads>,
-                        dim3((unsigned)tiles, (unsigned)plan.groups), kTileThreads, 0, stream, 0, p);
+        const dim3 grid((unsigned)tiles, (unsigned)plan.groups);
+        e = p.rows > (int64_t)lnorm::kSegment * plan.groups
+                ? moe::launch(lnorm::layer_norm_bwd_tile_kernel<E, P, VEC, kTileThreads, true>, grid, kTileThreads, 0, stream, 0, p)
+                : moe::launch(lnorm::layer_norm_bwd_tile_kernel<E, P, VEC, kTileThreads, false>, grid, kTileThreads, 0, stream, 0, p);
     } else {
         constexpr int kPack = 16 / E::kBytes;
         if constexpr (VEC == 1)

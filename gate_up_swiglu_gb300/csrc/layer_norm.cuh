@@ -974,39 +974,65 @@ __global__ void __launch_bounds__(T) layer_norm_bwd_sums_kernel(BwdParams p) {
     }
 }
 
-// blockIdx.x: the tile of T * VEC columns, blockIdx.y: the group of rows.
-template <typename E, typename P, int VEC, int T>
+// blockIdx.x: the tile of T * VEC columns, blockIdx.y: the group of rows.  Where the tiles are
+// many the groups are few (one from 156 thousand columns on that are not in packs).  SEGMENTS:
+// a group has more than kSegment rows, so its column sums are cut into segments of as many,
+// which are added up in their order (in every launch: [500, 70001] bf16 169 instead of 151 us).
+constexpr int kSegment = 256;
+
+template <typename E, typename P, int VEC, int T, bool SEGMENTS>
 __global__ void __launch_bounds__(T) layer_norm_bwd_tile_kernel(BwdParams p) {
     constexpr int EB = E::kBytes, B = EB * VEC, WN = B < 4 ? 1 : B / 4;
     swiglu::await_previous_grid();
     swiglu::allow_next_grid();
     const int64_t col = ((int64_t)blockIdx.x * T + threadIdx.x) * VEC;
     if (col >= p.n) return;
+    __shared__ float total[SEGMENTS ? 2 * VEC : 1][T];  // of the segments so far, out of the registers
+    if constexpr (SEGMENTS)
+#pragma unroll
+        for (int k = 0; k < 2 * VEC; ++k) total[k][threadIdx.x] = 0.0f;
     float q[VEC], aw[VEC], ab[VEC];
     if (p.w != nullptr) load_params<P, VEC>(p.w, col, q);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) aw[k] = ab[k] = 0.0f;
+    for (int64_t first = blockIdx.y; first < p.rows; first += (int64_t)kSegment * gridDim.y) {
+        const int64_t last = SEGMENTS ? min(p.rows, first + (int64_t)kSegment * gridDim.y) : p.rows;
 #pragma unroll 4
-    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
-        uint32_t xw[WN], dw[WN];
-        load_once<B>(p.x + row * p.x_stride + col * EB, xw);
-        load_once<B>(p.dy + row * p.dy_stride + col * EB, dw);
-        const float mean = p.mean[row], rstd = p.rstd[row], c1 = p.sums[2 * row],
-                    c2 = p.sums[2 * row + 1];
-        float v[VEC];
+        for (int64_t row = first; row < last; row += gridDim.y) {
+            uint32_t xw[WN], dw[WN];
+            load_once<B>(p.x + row * p.x_stride + col * EB, xw);
+            load_once<B>(p.dy + row * p.dy_stride + col * EB, dw);
+            const float mean = p.mean[row], rstd = p.rstd[row], c1 = p.sums[2 * row],
+                        c2 = p.sums[2 * row + 1];
+            float v[VEC];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            float xhat, dy;
-            unpack<E, VEC>(xw, dw, mean, rstd, k, xhat, dy);
-            aw[k] = fmaf(dy, xhat, aw[k]);
-            ab[k] += dy;
-            const float h = p.w != nullptr ? dy * q[k] : dy;
-            v[k] = rstd * fmaf(-xhat, c2, h - c1);
+            for (int k = 0; k < VEC; ++k) {
+                float xhat, dy;
+                unpack<E, VEC>(xw, dw, mean, rstd, k, xhat, dy);
+                aw[k] = fmaf(dy, xhat, aw[k]);
+                ab[k] += dy;
+                const float h = p.w != nullptr ? dy * q[k] : dy;
+                v[k] = rstd * fmaf(-xhat, c2, h - c1);
+            }
+            store_once<E, VEC>(p.dx + row * p.dx_stride + col * EB, v);
         }
-        store_once<E, VEC>(p.dx + row * p.dx_stride + col * EB, v);
+        if constexpr (SEGMENTS) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                total[k][threadIdx.x] += aw[k];
+                total[VEC + k][threadIdx.x] += ab[k];
+                aw[k] = ab[k] = 0.0f;
+            }
+        } else {
+            break;
+        }
     }
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
+        if constexpr (SEGMENTS) {
+            aw[k] = total[k][threadIdx.x];
+            ab[k] = total[VEC + k][threadIdx.x];
+        }
         emit<P, 1>(p, blockIdx.y, 0, col + k, aw + k);
         emit<P, 1>(p, blockIdx.y, 1, col + k, ab + k);
     }

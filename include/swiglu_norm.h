@@ -45,9 +45,12 @@ swiglu_status_t swiglu_layer_norm_fwd(const void *x, const void *w, const void *
  *   db = sum over rows of dy        (db may be NULL)
  * mean and rstd are those of the forward.  Row strides of dy, x and dx >= n.  The
  * column sums are fp32, in an order that depends on the sizes, the alignment and
- * the device alone: the same call gives the same bits.  (Every SM adds up 1 to 16
- * rows side by side, each chain some rows / (16 .. 1) / 152 long, and the chains are
- * added up after that.)  They take a workspace of
+ * the device alone: the same call gives the same bits.  (Rows are shared out among
+ * chains of additions: 16 on each SM up to 512 columns, 8, 4 and 2 up to 1024, 2048 and
+ * 4096, one up to 8192; two for each cluster of 4 CTAs, of 8 beyond 16384 columns, that
+ * the device runs at a time, 38 and 19 of them at most.  Beyond 32768 columns, where chains may
+ * be as few as one, they are cut into segments of 256 rows.  The segments and the chains of
+ * an SM, then the SMs' sums in 16 chains, are added up in their order.)  They take a workspace of
  * swiglu_layer_norm_bwd_workspace_size(rows, n, dtype) bytes, 16-byte aligned
  * (else SWIGLU_ERR_WORKSPACE), which may be used again by work later in the
  * stream, and not by work that runs at the same time.  Outputs and workspace

@@ -293,3 +293,17 @@ def test_backward_of_constant_rows_of_large_values(sw, rows, n, pad, dtype):
     within(dx, want[0], want[3], dtype, "dx")
     assert bool((dw == 0).all())
     within(db, want[2], want[5], dtype, "db")
+
+
+@pytest.mark.parametrize("n", [155651, 155652])
+def test_column_sums_of_many_very_long_rows(sw, n):
+    """Equal terms, whose rounding errors do not cancel: a chain over all 3000 rows would be
+    some 500 units off, segments are within the bound of every other length."""
+    rows = 3000
+    terms = torch.tensor([0.1, 0.3, 0.7, 1.1, 1.3, 0.013], device="cuda")[torch.arange(n, device="cuda") % 6]
+    dy, x = terms.repeat(rows, 1), torch.ones(1, n, device="cuda").repeat(rows, 1)
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dx, dw, db = sw.swiglu_layer_norm_bwd(dy, x, mean, rstd, torch.ones(n, device="cuda"), dx=torch.empty_like(x))
+    want = rows * terms.double()
+    for got in (dw, db):
+        within(got, want, (rows / 19 + 100) * U * want, F32, "sums")
