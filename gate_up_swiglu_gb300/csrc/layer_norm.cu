@@ -123,7 +123,7 @@ swiglu_status_t run_fwd_groups(const lnorm::FwdParams &p, int dev, int sms, swig
     constexpr int k = held_fwd(E::kBytes, VEC);
     const int64_t n = p.n;
     // fp32 parameters of bf16 rows stay in registers where a thread holds half as much
-    // ([8192, 4096] 30 us; read again for every row 38 us)
+    // ([8192, 4096] 35.0 us, [8192, 1024] 9.1 us; read again for every row 36.1 and 11.1 us)
     if constexpr (P::kBytes > E::kBytes) {
         constexpr int h = k / 2;
         if (n <= 32 * h / 2) return run_fwd<E, P, VEC, ANY, 32, h / 2>(p, dev, sms, stream);
@@ -196,10 +196,11 @@ Plan plan_bwd(int64_t rows, int64_t n, int vec, int period, int sms) {
         if (rows <= 4 * per_cta) return {g, 1, 1, false};
         return {g, 1, whole((rows + per_cta - 1) / per_cta, sms), any};
     }
-    // a cluster, with two rows at a time (three CTAs would take the room of four)
+    // a cluster of 4 or 8 CTAs, with two rows at a time (what two could hold, one does; three
+    // would take the room of four)
     // Of eight CTAs too few clusters run at a time to share every eighth row: there rows that
     // lie anywhere go element by element ([1000, 32761] bf16 102 us, in packs 138 us).
-    for (int c = 2; c <= kMaxCluster; c *= 2) {
+    for (int c = 4; c <= kMaxCluster; c *= 2) {
         const int64_t groups = (rows + 1) / 2;
         const int most = std::max(1, sms / c);
         if (n <= (int64_t)kClusterGroup * k * c)

@@ -85,7 +85,8 @@ __device__ __forceinline__ int64_t scale_offset(int64_t tile, int64_t i, int32_t
 // ---------------------------------------------------------------- kernels ---
 // Quantising and its inverse are one pass over the data: 2 (4) bytes an element on the
 // one side, 17/32 on the other, a few instructions an element: HBM bound.  [28672, 4096]
-// bf16 47 us (94 % of the copy rate), the inverse 45 us (98 %); [8192, 4095] 34 and 40 us.
+// bf16 46.5 us (94 % of the copy rate), the inverse 44.9 us (98 %).  Rows at any address pay
+// for their shifts and their ends: [8192, 4095] bf16 31 us (40 %) and 39 us (32 %).
 //
 // A thread takes eight or sixteen neighbouring elements (a pack) of kRows rows below
 // each other, so that what it costs to find its place comes once; 32 / VEC neighbouring

@@ -466,8 +466,9 @@ __global__ void __launch_bounds__(SplitShape<NT, TILES, PER_SM>::kThreads)
 // the lanes), up to three stages ahead of the products.  Copied by the MMA thread
 // (tcgen05.cp, as in the split kernel), each of a stage's six scale tiles held up the
 // products by some 47 cycles: [8192, 14336] x [4096, 14336] took 199 us, with four warps
-// 148 us (145 us now, 6.6 PFLOP/s).  What bounds it is what comes into an SM: 35.8 KB a
-// stage and CTA, 560 cycles at 64 bytes a cycle, where the products take less than a third.
+// 148 us (145 us now, 6.6 PFLOP/s; 151 us after seconds at the power limit).  A stage takes
+// some 740 cycles, of which the four products are 512: the tensor pipe is active 67 % of the time,
+// the port into an SM (35.8 KB a stage and CTA) 36 %.  Where the rest goes is not shown.
 //
 // Tensor memory has 512 columns: two accumulators of 256 leave no room for three
 // stages' scales, 24 columns each.  So the two overlap by 72 columns, and the epilogue
