@@ -1096,7 +1096,10 @@ constexpr int64_t kSms = 152;
 // What the two kernels take, in ns, fitted to times of [129 .. 2048] rows by [1000 ..
 // 28672] by [512 .. 14336]: a CTA of the split kernel takes one tile, its start and end
 // in full; a pair takes the next tile while it finishes one.  ([256, 14336] x [4096,
-// 14336] 13.4 and 24.0 us, [1024, 14336] x [4096, 14336] 27.4 and 24.4 us.)
+// 14336] 13.4 and 24.0 us, [1024, 14336] x [4096, 14336] 27.4 and 24.4 us.)  Beyond that range
+// it decides well for many rows by many columns (8192 x 1000 x 512 11.0 and 10.3 us, 4096 x
+// 4096 x 14336 101 and 83 us), and takes pairs too early below 129 rows (100 x 20000 x 256
+// 4.5 and 6.9 us) and for up to 256 columns (30000 x 100 x 300 7.3 and 18.7 us).
 int64_t split_cost(int64_t ctas, int tiles, int64_t stages) {
     if (tiles == 1 && ctas > kSms) return (ctas + 2 * kSms - 1) / (2 * kSms) * (300 * stages + 11000);  // two an SM
     return (ctas + kSms - 1) / kSms * (tiles == 1 ? 214 * stages + 5600 : 380 * stages + 6500);
