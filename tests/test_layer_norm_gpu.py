@@ -295,15 +295,19 @@ def test_backward_of_constant_rows_of_large_values(sw, rows, n, pad, dtype):
     within(db, want[2], want[5], dtype, "db")
 
 
-@pytest.mark.parametrize("n", [155651, 155652])
-def test_column_sums_of_many_very_long_rows(sw, n):
-    """Equal terms, whose rounding errors do not cancel: a chain over all 3000 rows would be
-    some 500 units off, segments are within the bound of every other length."""
-    rows = 3000
-    terms = torch.tensor([0.1, 0.3, 0.7, 1.1, 1.3, 0.013], device="cuda")[torch.arange(n, device="cuda") % 6]
-    dy, x = terms.repeat(rows, 1), torch.ones(1, n, device="cuda").repeat(rows, 1)
+@pytest.mark.parametrize("rows,n,dtype", [(3000, 155651, F32), (3000, 155652, F32), (600, 700009, BF16), (600, 700008, BF16)])
+def test_column_sums_of_many_very_long_rows(sw, rows, n, dtype):
+    """Equal terms, whose rounding errors do not cancel: a chain over 3000 rows would be some
+    500 units off, segments are within the bound of every other length."""
+    terms = torch.tensor([0.1, 0.3, 0.7, 1.1, 1.3, 0.013], device="cuda")[torch.arange(n, device="cuda") % 6].to(dtype)
+    dy, x = terms.repeat(rows, 1), torch.ones(1, n, device="cuda", dtype=dtype).repeat(rows, 1)
     mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
     dx, dw, db = sw.swiglu_layer_norm_bwd(dy, x, mean, rstd, torch.ones(n, device="cuda"), dx=torch.empty_like(x))
     want = rows * terms.double()
     for got in (dw, db):
         within(got, want, (rows / 19 + 100) * U * want, F32, "sums")
+    h = terms.double()
+    c1, c2 = h.mean(), h.mean()  # xhat = 1
+    off = U * (D * (h.abs().mean() + h.abs().mean()) + 8 * (h.abs() + c1.abs() + c2.abs()))
+    for r in (0, 255, 256, rows - 1):
+        within(dx[r], h - c1 - c2, off, dtype, "dx")
